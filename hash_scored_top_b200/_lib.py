@@ -21,6 +21,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _z = ctypes.c_size_t
+_l = ctypes.c_longlong
 
 # name -> (restype, argtypes); the order follows include/hash_scored_top.h
 SIGNATURES = {
@@ -48,6 +49,18 @@ SIGNATURES = {
     "socket_sparse_attend_paged": (_i, [_p, _p, _p, _i, _p, _i, _i, _i, _p, _i, _i, _i, _i, _i, _f, _p, _p, _z, _p]),
     "socket_decode_paged": (_i, [_p, _p, _p, _i, _p, _i, _i, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i,
                                  _f, _p, _p, _p, _z, _p]),
+    "quant_append": (_i, [_p, _p, _i, _l, _l, _l, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _i, _p, _p]),
+    "quant_read": (_i, [_p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _i, _p]),
+    "quant_decode": (_i, [_p, _i, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _z, _p]),
+    "quant_sparse_attend": (_i, [_p, _i, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _z, _p]),
+    "socket_decode_quant": (_i, [_p, _i, _p, _p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _f, _p, _p,
+                                 _p, _z, _p]),
+    "block_summarize": (_i, [_p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p]),
+    "block_select": (_i, [_p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _z, _p]),
+    "block_attend": (_i, [_p, _i, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _z, _p]),
+    "block_decode": (_i, [_p, _i, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p, _z,
+                          _p]),
+    "tree_decode": (_i, [_p, _i, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _i, _p, _z, _p]),
     "sk_workspace_bytes": (_z, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
     "sk_check_status": (_i, [_p]),
     "sk_profile_phases": (_i, [_p]),

@@ -20,10 +20,11 @@ import torch
 
 from . import _lib
 
-SK_F32, SK_BF16 = 0, 1
+SK_F32, SK_BF16, SK_INT8, SK_E4M3 = 0, 1, 2, 3
 (OP_HASH_KEYS, OP_SCORE, OP_TOPK, OP_SPARSE_ATTEND, OP_DECODE, OP_HATA_HASH, OP_HATA_DECODE, OP_DENSE_DECODE,
  OP_SELECT, OP_SOFT_COUNT, OP_DECODE_HEADS, OP_DECODE_ADAPTIVE, OP_DECODE_ADAPTIVE_HEADS, OP_SPARSE_ATTEND_PAGED,
- OP_DECODE_PAGED) = range(15)
+ OP_DECODE_PAGED, OP_QUANT_DECODE, OP_QUANT_SPARSE_ATTEND, OP_SOCKET_DECODE_QUANT, OP_BLOCK_SELECT, OP_BLOCK_ATTEND,
+ OP_BLOCK_DECODE, OP_TREE_DECODE) = range(22)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -476,3 +477,267 @@ def socket_soft_count_attend(Q, V, R, ids, idx, L: int, P: int, tau: float, O, w
 def check_status():
     """Synchronises the current stream and raises if a kernel flagged an error."""
     _check(_lib.lib.sk_check_status(_stream()), "sk_check_status")
+
+
+# ---------------------------------------------------------------- quantised caches, blocks, drafted tokens
+_CACHE_CODES = {torch.float32: SK_F32, torch.bfloat16: SK_BF16, torch.int8: SK_INT8, torch.float8_e4m3fn: SK_E4M3}
+
+
+def empty_quant(B: int, Hkv: int, Ncap: int, d: int, dtype=torch.int8, device="cuda"):
+    """A quantised cache (Kq, Vq, scales): two [B, Hkv, Ncap, d] of int8 or float8_e4m3fn and [B, Hkv, Ncap, 2] f32."""
+    if dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError(f"unsupported cache dtype {dtype} (int8 or float8_e4m3fn)")
+    Kq, Vq = (torch.zeros(B, Hkv, Ncap, d, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+    return Kq, Vq, torch.zeros(B, Hkv, Ncap, 2, dtype=torch.float32, device=device)
+
+
+def empty_block_summaries(B: int, Hkv: int, Ncap: int, d: int, block: int, device="cuda") -> torch.Tensor:
+    """Block summaries [B, Hkv, ceil(Ncap / block), 2, d] bf16: the keys' minima, then their maxima."""
+    return torch.zeros(B, Hkv, -(-Ncap // block), 2, d, dtype=torch.bfloat16, device=device)
+
+
+def tree_mask(seen: torch.Tensor) -> torch.Tensor:
+    """[B, T, T] bool (token t sees drafted key i) -> the words of tree_decode's mask [B, T, ceil(T / 32)] int32."""
+    B, T, _ = seen.shape
+    bits = torch.nn.functional.pad(seen, (0, -T % 32)).view(B, T, -1, 32).long()
+    w = (bits << torch.arange(32, device=seen.device)).sum(-1)
+    return torch.where(w >= 2**31, w - 2**32, w).to(torch.int32).contiguous()
+
+
+def _cache_code(t: torch.Tensor, quantised: bool = False) -> int:
+    code = _CACHE_CODES.get(t.dtype)
+    if code is None or (quantised and code < SK_INT8):
+        raise TypeError(f"unsupported cache dtype {t.dtype}")
+    return code
+
+
+def _on(first: torch.Tensor, *others):
+    """The device's guard: every tensor lies on `first`'s CUDA device, which the call makes current."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
+    return torch.cuda.device(dev)
+
+
+def _addr(t):
+    """Address of a contiguous tensor (its device was checked by _on), or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _want_cache(K, V, scales):
+    """Checks K, V and their scales; returns the cache's dtype code."""
+    code = _cache_code(K)
+    B, Hkv, Ncap, d = K.shape
+    if V is not None:
+        _want(V, K.dtype, K.shape, "V")
+    if code >= SK_INT8:
+        if scales is None:
+            raise ValueError("scales: a quantised cache needs them")
+        _want(scales, torch.float32, (B, Hkv, Ncap, 2), "scales")
+    elif scales is not None:
+        raise ValueError(f"scales: a {K.dtype} cache has none")
+    return code
+
+
+def _want_lens(lens, B, name="lens"):
+    if lens is not None:
+        _want(lens, torch.int32, (B,), name)
+
+
+def _raw_stream(t):
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _ws_arg(ws, op, device, *shape):
+    """The workspace's (tensor, address, bytes): the caller's as it is, or one of the size the library asks for."""
+    if ws is None:
+        ws = torch.empty(workspace_bytes(op, *shape), dtype=torch.uint8, device=device)
+    return ws, _addr(ws), ws.numel() * ws.element_size()
+
+
+def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, lens=None):
+    """Quantises K_new, V_new [B, Hkv, n, d] (f32 or bf16; any strides, the last dimension contiguous) into rows n_begin ..
+    (or starts[b] ..) of a quantised cache (see the C header)."""
+    B, Hkv, Ncap, d = Kq.shape
+    n = K_new.shape[2]
+    _cache_code(Kq, quantised=True)
+    code = _want_cache(Kq, Vq, scales)
+    _want(K_new, K_new.dtype, (B, Hkv, n, d), "K_new")
+    _want(V_new, K_new.dtype, (B, Hkv, n, d), "V_new")
+    _want_lens(starts, B, "starts")
+    _want_lens(lens, B)
+    if V_new.stride() != K_new.stride():
+        raise ValueError(f"V_new: strides {V_new.stride()}, expected K_new's {K_new.stride()}")
+    sb, sh, sn, sd = K_new.stride()
+    if sd != 1:
+        raise ValueError("K_new, V_new: the last dimension must be contiguous")
+    with _on(Kq, Vq, scales, K_new, V_new, starts, lens):
+        rc = _lib.lib.quant_append(K_new.data_ptr(), V_new.data_ptr(), _dtype_code(K_new), sb, sh, sn, _addr(starts), _addr(lens),
+                                   B, Hkv, Ncap, n_begin, n, d, _addr(Kq), _addr(Vq), code, _addr(scales), _raw_stream(Kq))
+    _check(rc, "quant_append")
+
+
+def quant_read(Kq, Vq, scales, K, V, n_begin: int = 0, starts=None, lens=None):
+    """Reads rows n_begin .. (or starts[b] ..) of a quantised cache back into K, V [B, Hkv, n, d] (f32 or bf16)."""
+    B, Hkv, Ncap, d = Kq.shape
+    n = K.shape[2]
+    _cache_code(Kq, quantised=True)
+    code = _want_cache(Kq, Vq, scales)
+    _want(K, K.dtype, (B, Hkv, n, d), "K")
+    _want(V, K.dtype, (B, Hkv, n, d), "V")
+    _want_lens(starts, B, "starts")
+    _want_lens(lens, B)
+    with _on(Kq, Vq, scales, K, V, starts, lens):
+        rc = _lib.lib.quant_read(_addr(Kq), _addr(Vq), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n,
+                                 d, _addr(K), _addr(V), _dtype_code(K), _raw_stream(Kq))
+    _check(rc, "quant_read")
+
+
+def quant_decode(Q, Kq, Vq, scales, N: int, scale: float, O, lens=None, ws=None):
+    """Dense decode attention over a quantised cache: O [B, Hq, d] f32 (see the C header)."""
+    B, Hq, d = Q.shape
+    _, Hkv, Ncap, _ = Kq.shape
+    _cache_code(Kq, quantised=True)
+    code = _want_cache(Kq, Vq, scales)
+    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _want(O, torch.float32, (B, Hq, d), "O")
+    _want_lens(lens, B)
+    with _on(Q, Kq, Vq, scales, O, lens, ws):
+        ws, w, wb = _ws_arg(ws, OP_QUANT_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d)
+        rc = _lib.lib.quant_decode(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(lens), B, Hq, Hkv,
+                                   Ncap, N, d, scale, _addr(O), w, wb, _raw_stream(Q))
+    _check(rc, "quant_decode")
+
+
+def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
+    """Attention over listed rows idx [B, Hkv, k] int32 (-1: none) of a quantised cache: O [B, Hq, d] f32."""
+    B, Hq, d = Q.shape
+    _, Hkv, Ncap, _ = Kq.shape
+    k = idx.shape[-1]
+    _cache_code(Kq, quantised=True)
+    code = _want_cache(Kq, Vq, scales)
+    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _want(idx, torch.int32, (B, Hkv, k), "idx")
+    _want(O, torch.float32, (B, Hq, d), "O")
+    with _on(Q, Kq, Vq, scales, idx, O, ws):
+        ws, w, wb = _ws_arg(ws, OP_QUANT_SPARSE_ATTEND, Q.device, B, Hq, Hkv, Ncap, k, d, 0, 0, k)
+        rc = _lib.lib.quant_sparse_attend(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(idx), B, Hq,
+                                          Hkv, Ncap, d, k, scale, _addr(O), w, wb, _raw_stream(Q))
+    _check(rc, "quant_sparse_attend")
+
+
+def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int, tau: float, k: int, scale: float, O,
+                        idx_out=None, ws=None):
+    """socket_decode over a quantised K/V cache (the hashed-key cache as there): O [B, Hq, d] f32."""
+    B, Hq, d = Q.shape
+    _, Hkv, Ncap, _ = Kq.shape
+    _cache_code(Kq, quantised=True)
+    code = _want_cache(Kq, Vq, scales)
+    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _want(R, torch.bfloat16, (L * P, d), "R")
+    _want(ids, torch.uint8, (B, Hkv, Ncap, ids_bytes_per_key(L)), "ids")
+    _want(norms, torch.float16, (B, Hkv, Ncap), "norms")
+    _want(O, torch.float32, (B, Hq, d), "O")
+    if idx_out is not None:
+        _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
+    with _on(Q, Kq, Vq, scales, R, ids, norms, O, idx_out, ws):
+        ws, w, wb = _ws_arg(ws, OP_SOCKET_DECODE_QUANT, Q.device, B, Hq, Hkv, Ncap, N, d, L, P, k)
+        rc = _lib.lib.socket_decode_quant(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(R), _addr(ids),
+                                          _addr(norms), B, Hq, Hkv, Ncap, N, d, L, P, tau, k, scale, _addr(O), _addr(idx_out), w,
+                                          wb, _raw_stream(Q))
+    _check(rc, "socket_decode_quant")
+
+
+def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None = None, scales=None, starts=None, lens=None):
+    """Summaries (per-channel minima and maxima) of the blocks that hold rows [n_begin, n_begin + n_count) of each pair."""
+    B, Hkv, Ncap, d = K.shape
+    n_count = Ncap - n_begin if n_count is None else n_count
+    code = _want_cache(K, None, scales)
+    _want(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
+    _want_lens(starts, B, "starts")
+    _want_lens(lens, B)
+    with _on(K, scales, bsum, starts, lens):
+        rc = _lib.lib.block_summarize(_addr(K), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n_count, d,
+                                      block, _addr(bsum), _raw_stream(K))
+    _check(rc, "block_summarize")
+
+
+def _block_shapes(Q, bsum, Ncap, block):
+    B, Hq, d = Q.shape
+    Hkv = bsum.shape[1]
+    _want(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
+    return B, Hq, Hkv, d
+
+
+def block_select(Q, bsum, Ncap: int, N: int, block: int, n_first: int, n_last: int, idx, lens=None, ws=None):
+    """The idx.shape[-1] blocks of each pair with the largest bounds: idx [B, Hkv, k] int32, ascending, then -1."""
+    B, Hq, Hkv, d = _block_shapes(Q, bsum, Ncap, block)
+    k = idx.shape[-1]
+    _want(idx, torch.int32, (B, Hkv, k), "idx")
+    _want_lens(lens, B)
+    with _on(Q, bsum, idx, lens, ws):
+        ws, w, wb = _ws_arg(ws, OP_BLOCK_SELECT, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+        rc = _lib.lib.block_select(_addr(Q), _dtype_code(Q), _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d, block, k, n_first,
+                                   n_last, _addr(idx), w, wb, _raw_stream(Q))
+    _check(rc, "block_select")
+
+
+def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None, lens=None, ws=None):
+    """Attention over the keys of the listed blocks idx [B, Hkv, k] int32 (-1: none): O [B, Hq, d] f32."""
+    B, Hq, d = Q.shape
+    _, Hkv, Ncap, _ = K.shape
+    k = idx.shape[-1]
+    code = _want_cache(K, V, scales)
+    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _want(idx, torch.int32, (B, Hkv, k), "idx")
+    _want(O, torch.float32, (B, Hq, d), "O")
+    _want_lens(lens, B)
+    with _on(Q, K, V, scales, idx, O, lens, ws):
+        ws, w, wb = _ws_arg(ws, OP_BLOCK_ATTEND, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+        rc = _lib.lib.block_attend(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(lens), _addr(idx), B,
+                                   Hq, Hkv, Ncap, N, d, block, k, scale, _addr(O), w, wb, _raw_stream(Q))
+    _check(rc, "block_attend")
+
+
+def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last: int, scale: float, O, scales=None, lens=None,
+                 idx_out=None, ws=None):
+    """block_select, then block_attend over its choice: O [B, Hq, d] f32; idx_out [B, Hkv, k] int32 if given."""
+    Ncap = K.shape[2]
+    B, Hq, Hkv, d = _block_shapes(Q, bsum, Ncap, block)
+    code = _want_cache(K, V, scales)
+    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _want(O, torch.float32, (B, Hq, d), "O")
+    if idx_out is not None:
+        _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
+    _want_lens(lens, B)
+    with _on(Q, K, V, scales, bsum, O, lens, idx_out, ws):
+        ws, w, wb = _ws_arg(ws, OP_BLOCK_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+        rc = _lib.lib.block_decode(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(bsum), _addr(lens), B,
+                                   Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, scale, _addr(O), _addr(idx_out), w, wb,
+                                   _raw_stream(Q))
+    _check(rc, "block_decode")
+
+
+def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=None, ws=None):
+    """Attention of T drafted tokens Q [B, T, Hq, d] over each sequence's cached keys and, under mask (tree_mask; None: a
+    chain), its drafted keys behind them: O [B, T, Hq, d] f32 or bf16 (see the C header)."""
+    B, T, Hq, d = Q.shape
+    _, Hkv, Ncap, _ = K.shape
+    code = _want_cache(K, V, scales)
+    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _want(O, O.dtype, (B, T, Hq, d), "O")
+    if mask is not None:
+        _want(mask, torch.int32, (B, T, -(-T // 32)), "mask")
+    _want_lens(lens, B)
+    with _on(Q, K, V, scales, O, mask, lens, ws):
+        ws, w, wb = _ws_arg(ws, OP_TREE_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, 0, 0, T)
+        rc = _lib.lib.tree_decode(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(lens), _addr(mask), B, T,
+                                  Hq, Hkv, Ncap, N, d, scale, _addr(O), _dtype_code(O), w, wb, _raw_stream(Q))
+    _check(rc, "tree_decode")

@@ -9,15 +9,16 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_NAME = "libhash_scored_top.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["csrc/api.cu"]
+SOURCES = ["csrc/api.cu", "csrc/cache_api.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
@@ -42,10 +43,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, *[os.path.join(HERE, s) for s in SOURCES]]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True, cwd=HERE)
+    with tempfile.TemporaryDirectory() as work:
+        objects = [os.path.join(work, f"{i}.o") for i in range(len(SOURCES))]
+        steps = [[nvcc, *NVCC_FLAGS, "-c", "-o", o, os.path.join(HERE, s)] for o, s in zip(objects, SOURCES)]
+        link = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objects]
+        if verbose:
+            print("\n".join(" ".join(c) for c in [*steps, link]), file=sys.stderr)
+        running = [subprocess.Popen(c, cwd=HERE) for c in steps]         # the sources compile side by side
+        for rc, c in [(p.wait(), c) for p, c in zip(running, steps)]:
+            if rc:
+                raise subprocess.CalledProcessError(rc, c)
+        subprocess.run(link, check=True, cwd=HERE)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/hash_scored_top.h"
+#include "host.cuh"
 #include "socket_kernels.cuh"
 #include "estimator.cuh"
 #include "adaptive.cuh"
@@ -23,11 +24,11 @@
 using namespace hst;
 
 namespace {
-
 thread_local std::string g_last_error = "no error";
 unsigned long long* g_phase_ts = nullptr;     // profiling hook, see sk_profile_phases
+}  // namespace
 
-int fail(int code, const char* fmt, ...) {
+int hst::fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -37,13 +38,7 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-int check_launch(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(SK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  return SK_OK;
-}
-
-cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+namespace {
 
 // Raises a kernel's dynamic shared-memory limit (and allows 16-CTA clusters)
 // once per kernel; later calls with the same or a smaller size skip the
@@ -79,53 +74,6 @@ cudaError_t set_kernel_smem(Kern kern, size_t smem, bool big_cluster = false) {
   return e;
 }
 
-constexpr int kMaxL = 64;
-constexpr int kNumSMs = 148;
-
-// Shapes common to the decode-side calls.
-int check_heads(int B, int Hq, int Hkv, int d) {
-  if (B < 1 || Hq < 1 || Hkv < 1) return fail(SK_ERR_INVALID_ARG, "B, Hq, Hkv must be >= 1");
-  if (Hq % Hkv) return fail(SK_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
-  if (d != 64 && d != 128) return fail(SK_ERR_UNSUPPORTED, "head dim d=%d: only 64 and 128 are supported", d);
-  return SK_OK;
-}
-
-int check_cache(int Ncap, int N) {
-  if (Ncap < 32 || Ncap % 32) return fail(SK_ERR_INVALID_ARG, "Ncap=%d must be a positive multiple of 32", Ncap);
-  if (N < 1 || N > Ncap) return fail(SK_ERR_INVALID_ARG, "N=%d must be in [1, Ncap=%d]", N, Ncap);
-  return SK_OK;
-}
-
-int check_tables(int L, int P, float tau) {
-  if (P < 1 || P > 8) return fail(SK_ERR_UNSUPPORTED, "P=%d: 1 <= P <= 8 (bucket IDs are bytes)", P);
-  if (L < 1 || L > kMaxL) return fail(SK_ERR_UNSUPPORTED, "L=%d: 1 <= L <= %d", L, kMaxL);
-  if (!(tau > 0.f)) return fail(SK_ERR_INVALID_ARG, "tau must be > 0");
-  return SK_OK;
-}
-
-int check_dtype(sk_dtype t) {
-  if (t != SK_F32 && t != SK_BF16) return fail(SK_ERR_INVALID_ARG, "unknown dtype %d", (int)t);
-  return SK_OK;
-}
-
-#define SK_TRY(expr)            \
-  do {                          \
-    const int _rc = (expr);     \
-    if (_rc != SK_OK) return _rc; \
-  } while (0)
-
-#define SK_NONNULL(ptr)                                                          \
-  do {                                                                           \
-    if ((ptr) == nullptr) return fail(SK_ERR_INVALID_ARG, "%s is NULL", #ptr);   \
-  } while (0)
-
-// Alignment the kernels' vector loads and bulk copies rely on.
-#define SK_ALIGNED(ptr, bytes)                                                                   \
-  do {                                                                                           \
-    if (reinterpret_cast<uintptr_t>(ptr) % (bytes))                                              \
-      return fail(SK_ERR_INVALID_ARG, "%s must be %d-byte aligned", #ptr, (int)(bytes));         \
-  } while (0)
-
 // ---------------------------------------------------------------- plans
 // Splits over keys of the attention kernel: one wave of ~2 CTAs per SM
 // (sparse) or several waves (dense), at least 16 keys each.
@@ -137,8 +85,6 @@ int attend_splits(int n, int pairs, bool dense) {
   if (splits > max_splits) splits = max_splits;
   return splits < 1 ? 1 : splits;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of the attention kernel: partials, then one counter per pair.
 size_t attend_ws_bytes(int pairs, int splits, int G, int d) {
@@ -1547,6 +1493,37 @@ int socket_decode_paged(const void* Q, const void* K_pool, const void* V_pool, s
                            scale, O, w + list_bytes + sel, ws_bytes - list_bytes - sel, s);
 }
 
+int socket_decode_quant(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                        const void* R, const void* ids, const void* norms, int B, int Hq, int Hkv, int Ncap, int N,
+                        int d, int L, int P, float tau, int k, float scale, float* O, int* idx_out, void* ws,
+                        size_t ws_bytes, void* stream) {
+  SK_NONNULL(R);
+  SK_NONNULL(ids);
+  SK_NONNULL(norms);
+  SK_ALIGNED(R, 16);
+  SK_ALIGNED(ids, 32);
+  SK_ALIGNED(norms, 2);
+  SK_TRY(quant_list_check(Q, q, Kq, Vq, kv, scales, B, Hq, Hkv, Ncap, d, k, O));
+  SK_TRY(check_cache(Ncap, N));
+  SK_TRY(check_tables(L, P, tau));
+  if (k > N) return fail(SK_ERR_INVALID_ARG, "k=%d must be in [1, N=%d]", k, N);
+  const int pairs = B * Hkv;
+  const FusedPlan fp = plan_select(pairs, N, k, Hq / Hkv, d, L, P, false, max_cluster_size());
+  const size_t list_bytes = align256((size_t)pairs * k * 4);
+  const size_t sel = align256(select_ws_bytes(fp, pairs, Ncap, L));
+  const size_t need = list_bytes + sel + cache_workspace_bytes(SK_OP_QUANT_SPARSE_ATTEND, B, Hq, Hkv, Ncap, N, d, 0, k);
+  if (ws == nullptr || ws_bytes < need)
+    return fail(SK_ERR_WORKSPACE, "workspace: need %zu bytes, got %zu", need, ws == nullptr ? (size_t)0 : ws_bytes);
+  SK_ALIGNED(ws, 16);
+  char* w = reinterpret_cast<char*>(ws);
+  int* idx = idx_out ? idx_out : reinterpret_cast<int*>(w);
+  const cudaStream_t s = as_stream(stream);
+  SK_TRY(decode_impl(Q, nullptr, nullptr, q, R, ids, norms, B, Hq, Hkv, Ncap, N, d, L, P, tau, k, 0.f, nullptr, idx,
+                     w + list_bytes, sel, false, false, s));
+  return quant_list_launch(Q, q, Kq, Vq, kv, scales, idx, B, Hq, Hkv, Ncap, d, k, scale, O, w + list_bytes + sel, s,
+                           fp.C > 0);
+}
+
 int hata_hash_keys(const void* K, sk_dtype kv, const void* R128, int B, int Hkv, int Ncap, int n_begin, int n_count,
                    int d, void* codes, void* stream) {
   SK_NONNULL(K);
@@ -1737,8 +1714,15 @@ size_t sk_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int N, int d
       if (k < 1 || N < 1 || Hq / Hu > 8 || L < 1 || L > kMaxL || P < 1 || P > 8) return bad;
       return adaptive_ws_bytes(B, Hq, Hu, Ncap, d, L, k);
     }
+    case SK_OP_SOCKET_DECODE_QUANT: {
+      if (k < 1 || N < 1 || G > 8 || L < 1 || L > kMaxL || P < 1 || P > 8) return bad;
+      const size_t at = cache_workspace_bytes(SK_OP_QUANT_SPARSE_ATTEND, B, Hq, Hkv, Ncap, N, d, 0, k);
+      if (at == bad) return bad;
+      const FusedPlan fp = plan_select(pairs, N, k, G, d, L, P, false, 8);
+      return align256((size_t)pairs * k * 4) + align256(select_ws_bytes(fp, pairs, Ncap, L)) + at;
+    }
     default:
-      return bad;
+      return cache_workspace_bytes(op, B, Hq, Hkv, Ncap, N, d, L, k);
   }
 }
 
@@ -1763,9 +1747,17 @@ int sk_check_status(void* stream) {
   if (word) {
     const unsigned int zero = 0;
     cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+  }
+  unsigned int cache_word = 0;
+  e = cache_take_error(&cache_word);
+  if (e != cudaSuccess) return fail(SK_ERR_CUDA, "error word: %s", cudaGetErrorString(e));
+  word |= cache_word;
+  if (word) {
     if (word & ERR_TIMEOUT) return fail(SK_ERR_TIMEOUT, "a device-side bounded wait gave up");
     if (word & ERR_RANGE)
       return fail(SK_ERR_INVALID_ARG, "a page-table entry was outside [0, num_pages); its rows were read from page 0");
+    if (word & ERR_ROWS)
+      return fail(SK_ERR_INVALID_ARG, "a row to append lay outside [0, Ncap); it was not written");
     return fail(SK_ERR_UNSUPPORTED, "a kernel's shared-memory plan did not fit; it wrote nothing");
   }
   return SK_OK;

@@ -1,0 +1,489 @@
+// C ABI of the operators over quantised, block-selected and drafted caches:
+// argument validation, launch planning and launches, under the rules of
+// api.cu (everything is checked on the host before anything is launched,
+// nothing is allocated, all work is asynchronous on the caller's stream).
+#include <algorithm>
+#include <climits>
+
+#include "host.cuh"
+#include "blocks.cuh"
+#include "cache_attend.cuh"
+#include "quant.cuh"
+
+using namespace hst;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A kernel launch, as the programmatic dependent of the kernel before it on
+// the stream if `pdl` (it waits before it reads what that kernel writes).
+template <typename Params>
+int launch(void (*kern)(Params), dim3 grid, int threads, size_t smem, cudaStream_t s, bool pdl, const char* what,
+           const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return fail(SK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
+// ---------------------------------------------------------------- checks
+bool is_8bit(int kv) { return kv == SK_INT8 || kv == SK_E4M3; }
+
+int check_8bit(sk_dtype kv) {
+  if (!is_8bit(kv)) return fail(SK_ERR_INVALID_ARG, "cache dtype %d: SK_INT8 or SK_E4M3 expected", (int)kv);
+  return SK_OK;
+}
+
+// Any format of cache, its scales, and a query type that goes with it.
+int check_formats(sk_dtype q, sk_dtype kv, const float* scales) {
+  SK_TRY(check_dtype(q));
+  if (is_8bit(kv)) {
+    SK_NONNULL(scales);
+    SK_ALIGNED(scales, 8);
+    return SK_OK;
+  }
+  SK_TRY(check_dtype(kv));
+  if (q != kv) return fail(SK_ERR_INVALID_ARG, "Q has dtype %d, the cache %d: they must be the same", (int)q, (int)kv);
+  return SK_OK;
+}
+
+int check_grid(int B, int Hq, int Hkv, int d) {
+  SK_TRY(check_heads(B, Hq, Hkv, d));
+  if ((long long)B * Hkv > 65535) return fail(SK_ERR_UNSUPPORTED, "B * Hkv = %lld > 65535", (long long)B * Hkv);
+  if (Hq / Hkv > 8) return fail(SK_ERR_UNSUPPORTED, "group size G=%d > 8", Hq / Hkv);
+  return SK_OK;
+}
+
+int check_ncap(int Ncap) {
+  if (Ncap < 32 || Ncap % 32) return fail(SK_ERR_INVALID_ARG, "Ncap=%d must be a positive multiple of 32", Ncap);
+  return SK_OK;
+}
+
+int check_rows(const int* starts, int Ncap, int n_begin, int n_count) {
+  SK_TRY(check_ncap(Ncap));
+  if (n_count < 0) return fail(SK_ERR_INVALID_ARG, "n_count=%d must be >= 0", n_count);
+  if (starts == nullptr && (n_begin < 0 || (long long)n_begin + n_count > Ncap))
+    return fail(SK_ERR_INVALID_ARG, "key range [%d, %d+%d) outside [0, Ncap=%d)", n_begin, n_begin, n_count, Ncap);
+  return SK_OK;
+}
+
+int check_block(int block) {
+  if (block != 16 && block != 32 && block != 64 && block != 128)
+    return fail(SK_ERR_UNSUPPORTED, "block=%d: 16, 32, 64 or 128 keys", block);
+  return SK_OK;
+}
+
+int check_ws(const void* ws, size_t got, size_t need) {
+  if (need > 0 && (ws == nullptr || got < need))
+    return fail(SK_ERR_WORKSPACE, "workspace: need %zu bytes, got %zu", need, ws == nullptr ? (size_t)0 : got);
+  SK_ALIGNED(ws, 16);
+  return SK_OK;
+}
+
+// ---------------------------------------------------------------- attention
+// Splits of a pair's positions: about four blocks per SM over all rows.
+int rows_splits(int pairs, int R, int n) {
+  const long long rows = (long long)pairs * R;
+  const long long want = (4LL * kNumSMs + rows - 1) / rows;
+  return (int)std::max(1LL, std::min(want, (long long)(n + 63) / 64));
+}
+
+size_t attend_bytes(int pairs, int R, int n, int d) {
+  return align256((size_t)pairs * R * rows_splits(pairs, R, n) * (d + 2) * sizeof(float));
+}
+
+template <int D>
+int launch_rows(const CacheAttendParams& p, sk_dtype kv, int pairs, bool pdl, cudaStream_t s) {
+  const dim3 grid(p.splits, p.T * p.G, pairs);
+  auto kern = kv == SK_F32    ? cache_attend_rows_kernel<D, KV_F32>
+              : kv == SK_BF16 ? cache_attend_rows_kernel<D, KV_BF16>
+              : kv == SK_INT8 ? cache_attend_rows_kernel<D, KV_INT8>
+                              : cache_attend_rows_kernel<D, KV_E4M3>;
+  return launch(kern, grid, CACHE_THREADS, 0, s, pdl, "cache_attend_rows_kernel", p);
+}
+
+// Attention over the positions that `p` describes (all of it but part, splits
+// and the query's place), then the merge of its splits into O.
+int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float scale, void* O, sk_dtype o, void* ws,
+           bool pdl, cudaStream_t s) {
+  const int pairs = B * p.Hkv, R = p.T * p.G;
+  p.q_bf16 = q == SK_BF16;
+  p.scale_log2 = scale * kLog2e;
+  p.part = reinterpret_cast<float*>(ws);
+  p.splits = rows_splits(pairs, R, p.n);
+  SK_TRY(d == 128 ? launch_rows<128>(p, kv, pairs, pdl, s) : launch_rows<64>(p, kv, pairs, pdl, s));
+  CacheMergeParams m;
+  m.part = p.part;
+  m.O = O;
+  m.Hq = p.Hq;
+  m.Hkv = p.Hkv;
+  m.T = p.T;
+  m.G = p.G;
+  m.splits = p.splits;
+  auto merge = d == 128 ? (o == SK_BF16 ? cache_merge_kernel<128, __nv_bfloat16> : cache_merge_kernel<128, float>)
+                        : (o == SK_BF16 ? cache_merge_kernel<64, __nv_bfloat16> : cache_merge_kernel<64, float>);
+  return launch(merge, dim3(R, pairs), d, 0, s, true, "cache_merge_kernel", m);
+}
+
+CacheAttendParams cache_params(const void* Q, const void* K, const void* V, const float* scales, const int* lens, int Hq,
+                               int Hkv, int Ncap, int N) {
+  CacheAttendParams p = {};
+  p.Q = Q;
+  p.K = K;
+  p.V = V;
+  p.scales = scales;
+  p.lens = lens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.T = 1;
+  p.G = Hq / Hkv;
+  p.Ncap = Ncap;
+  p.N = N;
+  return p;
+}
+
+// ---------------------------------------------------------------- blocks
+int num_blocks(int Ncap, int block) { return (Ncap + block - 1) / block; }
+
+size_t select_bytes(int pairs, int Ncap, int block) { return align256((size_t)pairs * num_blocks(Ncap, block) * 4); }
+
+int check_select(const void* Q, sk_dtype q, const void* bsum, int B, int Hq, int Hkv, int Ncap, int N, int d, int block,
+                 int k, int n_first, int n_last) {
+  SK_NONNULL(Q);
+  SK_NONNULL(bsum);
+  SK_ALIGNED(Q, 16);
+  SK_ALIGNED(bsum, 16);
+  SK_TRY(check_dtype(q));
+  SK_TRY(check_grid(B, Hq, Hkv, d));
+  SK_TRY(check_cache(Ncap, N));
+  SK_TRY(check_block(block));
+  if (k < 1 || (long long)k * block > INT_MAX) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
+  if (n_first < 0 || n_last < 0 || (long long)n_first + n_last > k)
+    return fail(SK_ERR_INVALID_ARG, "n_first=%d and n_last=%d must be >= 0 and at most k=%d together", n_first, n_last, k);
+  return SK_OK;
+}
+
+int select_impl(const void* Q, sk_dtype q, const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N,
+                int d, int block, int k, int n_first, int n_last, int* idx, void* ws, cudaStream_t s) {
+  BlockSelectParams p;
+  p.Q = Q;
+  p.bsum = reinterpret_cast<const __nv_bfloat16*>(bsum);
+  p.lens = lens;
+  p.keys = reinterpret_cast<uint32_t*>(ws);
+  p.idx = idx;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.NB = num_blocks(Ncap, block);
+  p.N = N;
+  p.block = block;
+  p.k = k;
+  p.n_first = n_first;
+  p.n_last = n_last;
+  const int pairs = B * Hkv, warps = BSCORE_THREADS / 32;
+  const int chunks = std::max(1, std::min((num_blocks(N, block) + warps - 1) / warps, (8 * kNumSMs + pairs - 1) / pairs));
+  auto score = d == 128 ? (q == SK_BF16 ? block_score_kernel<128, __nv_bfloat16> : block_score_kernel<128, float>)
+                        : (q == SK_BF16 ? block_score_kernel<64, __nv_bfloat16> : block_score_kernel<64, float>);
+  SK_TRY(launch(score, dim3(chunks, pairs), BSCORE_THREADS, 0, s, false, "block_score_kernel", p));
+  return launch(block_topk_kernel, dim3(pairs), BTOPK_THREADS, 0, s, true, "block_topk_kernel", p);
+}
+
+int check_cache_args(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales, int B,
+                     int Hq, int Hkv, int Ncap, int d, const void* O) {
+  SK_NONNULL(Q);
+  SK_NONNULL(K);
+  SK_NONNULL(V);
+  SK_NONNULL(O);
+  SK_ALIGNED(Q, 16);
+  SK_ALIGNED(K, 16);
+  SK_ALIGNED(V, 16);
+  SK_ALIGNED(O, 16);
+  SK_TRY(check_formats(q, kv, scales));
+  SK_TRY(check_grid(B, Hq, Hkv, d));
+  return check_ncap(Ncap);
+}
+
+int block_attend_impl(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                      const int* lens, const int* idx, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k,
+                      float scale, float* O, void* ws, bool pdl, cudaStream_t s) {
+  CacheAttendParams p = cache_params(Q, K, V, scales, lens, Hq, Hkv, Ncap, N);
+  p.mode = KEYS_BLOCKS;
+  p.idx = idx;
+  p.k = k;
+  p.block = block;
+  p.n = k * block;
+  return attend(p, q, kv, B, d, scale, O, SK_F32, ws, pdl, s);
+}
+
+constexpr int kMaxDrafts = 256;
+
+}  // namespace
+
+// ---------------------------------------------------------------- for api.cu
+size_t hst::cache_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k) {
+  const size_t bad = (size_t)-1;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 8 || (long long)B * Hkv > 65535 || (d != 64 && d != 128))
+    return bad;
+  const int pairs = B * Hkv, G = Hq / Hkv;
+  switch (op) {
+    case SK_OP_QUANT_DECODE:
+      return N < 1 ? bad : attend_bytes(pairs, G, N, d);
+    case SK_OP_QUANT_SPARSE_ATTEND:
+      return k < 1 ? bad : attend_bytes(pairs, G, k, d);
+    case SK_OP_BLOCK_SELECT:
+    case SK_OP_BLOCK_ATTEND:
+    case SK_OP_BLOCK_DECODE: {
+      if (k < 1 || Ncap < 32 || (block != 16 && block != 32 && block != 64 && block != 128) ||
+          (long long)k * block > INT_MAX)
+        return bad;
+      if (op == SK_OP_BLOCK_SELECT) return select_bytes(pairs, Ncap, block);
+      const size_t at = attend_bytes(pairs, G, k * block, d);
+      if (op == SK_OP_BLOCK_ATTEND) return at;
+      return select_bytes(pairs, Ncap, block) + align256((size_t)pairs * k * 4) + at;
+    }
+    case SK_OP_TREE_DECODE:
+      if (k < 1 || k > kMaxDrafts || N < 0 || N > INT_MAX - k) return bad;
+      return attend_bytes(pairs, k * G, N + k, d);
+    default:
+      return bad;
+  }
+}
+
+cudaError_t hst::cache_take_error(unsigned int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_error_word, sizeof(*word));
+  if (e == cudaSuccess && *word) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+  }
+  return e;
+}
+
+int hst::quant_list_check(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                          int B, int Hq, int Hkv, int Ncap, int d, int k, const float* O) {
+  SK_NONNULL(Kq);
+  SK_NONNULL(Vq);
+  SK_TRY(check_8bit(kv));
+  SK_TRY(check_cache_args(Q, q, Kq, Vq, kv, scales, B, Hq, Hkv, Ncap, d, O));
+  if (k < 1) return fail(SK_ERR_INVALID_ARG, "k=%d must be >= 1", k);
+  return SK_OK;
+}
+
+int hst::quant_list_launch(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                           const int* idx, int B, int Hq, int Hkv, int Ncap, int d, int k, float scale, float* O,
+                           void* ws, cudaStream_t s, bool pdl) {
+  CacheAttendParams p = cache_params(Q, Kq, Vq, scales, nullptr, Hq, Hkv, Ncap, Ncap);
+  p.mode = KEYS_LISTED;
+  p.idx = idx;
+  p.k = k;
+  p.n = k;
+  return attend(p, q, kv, B, d, scale, O, SK_F32, ws, pdl, s);
+}
+
+extern "C" {
+
+int quant_append(const void* K_new, const void* V_new, sk_dtype src, long long stride_b, long long stride_h,
+                 long long stride_n, const int* starts, const int* lens, int B, int Hkv, int Ncap, int n_begin,
+                 int n_count, int d, void* Kq, void* Vq, sk_dtype kv, float* scales, void* stream) {
+  SK_NONNULL(K_new);
+  SK_NONNULL(V_new);
+  SK_NONNULL(Kq);
+  SK_NONNULL(Vq);
+  SK_NONNULL(scales);
+  SK_ALIGNED(K_new, 16);
+  SK_ALIGNED(V_new, 16);
+  SK_ALIGNED(Kq, 16);
+  SK_ALIGNED(Vq, 16);
+  SK_ALIGNED(scales, 8);
+  SK_TRY(check_dtype(src));
+  SK_TRY(check_8bit(kv));
+  SK_TRY(check_grid(B, Hkv, Hkv, d));
+  SK_TRY(check_rows(starts, Ncap, n_begin, n_count));
+  const long long per16 = src == SK_BF16 ? 8 : 4;
+  if (stride_b % per16 || stride_h % per16 || stride_n % per16)
+    return fail(SK_ERR_INVALID_ARG, "strides (%lld, %lld, %lld) must be multiples of 16 bytes (%lld elements)", stride_b,
+                stride_h, stride_n, per16);
+  if (n_count == 0) return SK_OK;
+  QuantParams p = {};
+  p.src[0] = K_new;
+  p.src[1] = V_new;
+  p.sb = stride_b;
+  p.sh = stride_h;
+  p.sn = stride_n;
+  p.codes[0] = Kq;
+  p.codes[1] = Vq;
+  p.scales = scales;
+  p.rows = {starts, lens, n_begin, n_count, Ncap};
+  p.Hkv = Hkv;
+  p.pairs = B * Hkv;
+  const int per_block = QUANT_THREADS / (2 * (d / 8)) * QUANT_UNROLL;
+  auto kern = d == 128 ? (src == SK_BF16 ? (kv == SK_INT8 ? quant_append_kernel<128, __nv_bfloat16, KV_INT8>
+                                                         : quant_append_kernel<128, __nv_bfloat16, KV_E4M3>)
+                                         : (kv == SK_INT8 ? quant_append_kernel<128, float, KV_INT8>
+                                                         : quant_append_kernel<128, float, KV_E4M3>))
+                       : (src == SK_BF16 ? (kv == SK_INT8 ? quant_append_kernel<64, __nv_bfloat16, KV_INT8>
+                                                         : quant_append_kernel<64, __nv_bfloat16, KV_E4M3>)
+                                         : (kv == SK_INT8 ? quant_append_kernel<64, float, KV_INT8>
+                                                         : quant_append_kernel<64, float, KV_E4M3>));
+  return launch(kern, dim3((n_count + per_block - 1) / per_block, B * Hkv), QUANT_THREADS, 0, as_stream(stream), false,
+                "quant_append_kernel", p);
+}
+
+int quant_read(const void* Kq, const void* Vq, sk_dtype kv, const float* scales, const int* starts, const int* lens,
+               int B, int Hkv, int Ncap, int n_begin, int n_count, int d, void* K, void* V, sk_dtype dst, void* stream) {
+  SK_NONNULL(Kq);
+  SK_NONNULL(Vq);
+  SK_NONNULL(scales);
+  SK_NONNULL(K);
+  SK_NONNULL(V);
+  SK_ALIGNED(Kq, 16);
+  SK_ALIGNED(Vq, 16);
+  SK_ALIGNED(scales, 8);
+  SK_ALIGNED(K, 16);
+  SK_ALIGNED(V, 16);
+  SK_TRY(check_8bit(kv));
+  SK_TRY(check_dtype(dst));
+  SK_TRY(check_grid(B, Hkv, Hkv, d));
+  SK_TRY(check_rows(starts, Ncap, n_begin, n_count));
+  if (n_count == 0) return SK_OK;
+  QuantParams p = {};
+  p.codes[0] = const_cast<void*>(Kq);
+  p.codes[1] = const_cast<void*>(Vq);
+  p.scales = const_cast<float*>(scales);
+  p.dst[0] = K;
+  p.dst[1] = V;
+  p.rows = {starts, lens, n_begin, n_count, Ncap};
+  p.Hkv = Hkv;
+  p.pairs = B * Hkv;
+  const int per_block = QUANT_THREADS / (2 * (d / 8)) * QUANT_UNROLL;
+  auto kern = d == 128 ? (dst == SK_BF16 ? (kv == SK_INT8 ? quant_read_kernel<128, __nv_bfloat16, KV_INT8>
+                                                         : quant_read_kernel<128, __nv_bfloat16, KV_E4M3>)
+                                         : (kv == SK_INT8 ? quant_read_kernel<128, float, KV_INT8>
+                                                         : quant_read_kernel<128, float, KV_E4M3>))
+                       : (dst == SK_BF16 ? (kv == SK_INT8 ? quant_read_kernel<64, __nv_bfloat16, KV_INT8>
+                                                         : quant_read_kernel<64, __nv_bfloat16, KV_E4M3>)
+                                         : (kv == SK_INT8 ? quant_read_kernel<64, float, KV_INT8>
+                                                         : quant_read_kernel<64, float, KV_E4M3>));
+  return launch(kern, dim3((n_count + per_block - 1) / per_block, B * Hkv), QUANT_THREADS, 0, as_stream(stream), false,
+                "quant_read_kernel", p);
+}
+
+int quant_decode(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                 const int* lens, int B, int Hq, int Hkv, int Ncap, int N, int d, float scale, float* O, void* ws,
+                 size_t ws_bytes, void* stream) {
+  SK_TRY(check_8bit(kv));
+  SK_TRY(check_cache_args(Q, q, Kq, Vq, kv, scales, B, Hq, Hkv, Ncap, d, O));
+  SK_TRY(check_cache(Ncap, N));
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_QUANT_DECODE, B, Hq, Hkv, Ncap, N, d, 0, 0)));
+  CacheAttendParams p = cache_params(Q, Kq, Vq, scales, lens, Hq, Hkv, Ncap, N);
+  p.mode = KEYS_ALL;
+  p.n = N;
+  return attend(p, q, kv, B, d, scale, O, SK_F32, ws, false, as_stream(stream));
+}
+
+int quant_sparse_attend(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                        const int* idx, int B, int Hq, int Hkv, int Ncap, int d, int k, float scale, float* O, void* ws,
+                        size_t ws_bytes, void* stream) {
+  SK_NONNULL(idx);
+  SK_TRY(quant_list_check(Q, q, Kq, Vq, kv, scales, B, Hq, Hkv, Ncap, d, k, O));
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_QUANT_SPARSE_ATTEND, B, Hq, Hkv, Ncap, 0, d, 0, k)));
+  return quant_list_launch(Q, q, Kq, Vq, kv, scales, idx, B, Hq, Hkv, Ncap, d, k, scale, O, ws, as_stream(stream), false);
+}
+
+int block_summarize(const void* K, sk_dtype kv, const float* scales, const int* starts, const int* lens, int B, int Hkv,
+                    int Ncap, int n_begin, int n_count, int d, int block, void* bsum, void* stream) {
+  SK_NONNULL(K);
+  SK_NONNULL(bsum);
+  SK_ALIGNED(K, 16);
+  SK_ALIGNED(bsum, 16);
+  SK_TRY(check_formats(kv == SK_F32 ? SK_F32 : SK_BF16, kv, scales));
+  SK_TRY(check_grid(B, Hkv, Hkv, d));
+  SK_TRY(check_block(block));
+  SK_TRY(check_rows(starts, Ncap, n_begin, n_count));
+  if (n_count == 0) return SK_OK;
+  SummaryParams p;
+  p.K = K;
+  p.scales = scales;
+  p.bsum = reinterpret_cast<__nv_bfloat16*>(bsum);
+  p.rows = {starts, lens, n_begin, n_count, Ncap};
+  p.Hkv = Hkv;
+  p.NB = num_blocks(Ncap, block);
+  p.block = block;
+  // n_count rows lie in at most this many blocks, wherever they start
+  const int most = std::min((int)(((long long)n_count + block - 2) / block + 1), p.NB);
+  const int warps = SUMMARY_THREADS / 32;
+  auto kern = d == 128 ? (kv == SK_F32    ? block_summarize_kernel<128, KV_F32>
+                          : kv == SK_BF16 ? block_summarize_kernel<128, KV_BF16>
+                          : kv == SK_INT8 ? block_summarize_kernel<128, KV_INT8>
+                                          : block_summarize_kernel<128, KV_E4M3>)
+                       : (kv == SK_F32    ? block_summarize_kernel<64, KV_F32>
+                          : kv == SK_BF16 ? block_summarize_kernel<64, KV_BF16>
+                          : kv == SK_INT8 ? block_summarize_kernel<64, KV_INT8>
+                                          : block_summarize_kernel<64, KV_E4M3>);
+  return launch(kern, dim3((most + warps - 1) / warps, B * Hkv), SUMMARY_THREADS, 0, as_stream(stream), false,
+                "block_summarize_kernel", p);
+}
+
+int block_select(const void* Q, sk_dtype q, const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N,
+                 int d, int block, int k, int n_first, int n_last, int* idx, void* ws, size_t ws_bytes, void* stream) {
+  SK_TRY(check_select(Q, q, bsum, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last));
+  SK_NONNULL(idx);
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_BLOCK_SELECT, B, Hq, Hkv, Ncap, N, d, block, k)));
+  return select_impl(Q, q, bsum, lens, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, idx, ws, as_stream(stream));
+}
+
+int block_attend(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                 const int* lens, const int* idx, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k,
+                 float scale, float* O, void* ws, size_t ws_bytes, void* stream) {
+  SK_NONNULL(idx);
+  SK_TRY(check_cache_args(Q, q, K, V, kv, scales, B, Hq, Hkv, Ncap, d, O));
+  SK_TRY(check_cache(Ncap, N));
+  SK_TRY(check_block(block));
+  if (k < 1 || (long long)k * block > INT_MAX) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_BLOCK_ATTEND, B, Hq, Hkv, Ncap, N, d, block, k)));
+  return block_attend_impl(Q, q, K, V, kv, scales, lens, idx, B, Hq, Hkv, Ncap, N, d, block, k, scale, O, ws, false,
+                           as_stream(stream));
+}
+
+int block_decode(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                 const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k,
+                 int n_first, int n_last, float scale, float* O, int* idx_out, void* ws, size_t ws_bytes, void* stream) {
+  SK_TRY(check_cache_args(Q, q, K, V, kv, scales, B, Hq, Hkv, Ncap, d, O));
+  SK_TRY(check_select(Q, q, bsum, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last));
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_BLOCK_DECODE, B, Hq, Hkv, Ncap, N, d, block, k)));
+  const cudaStream_t s = as_stream(stream);
+  char* w = reinterpret_cast<char*>(ws);
+  const size_t sel = select_bytes(B * Hkv, Ncap, block);
+  int* idx = idx_out ? idx_out : reinterpret_cast<int*>(w + sel);
+  SK_TRY(select_impl(Q, q, bsum, lens, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, idx, w, s));
+  return block_attend_impl(Q, q, K, V, kv, scales, lens, idx, B, Hq, Hkv, Ncap, N, d, block, k, scale, O,
+                           w + sel + align256((size_t)B * Hkv * k * 4), true, s);
+}
+
+int tree_decode(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                const int* lens, const int* mask, int B, int T, int Hq, int Hkv, int Ncap, int N, int d, float scale,
+                void* O, sk_dtype o, void* ws, size_t ws_bytes, void* stream) {
+  SK_TRY(check_cache_args(Q, q, K, V, kv, scales, B, Hq, Hkv, Ncap, d, O));
+  SK_TRY(check_dtype(o));
+  if (T < 1 || T > kMaxDrafts) return fail(SK_ERR_UNSUPPORTED, "T=%d: 1 <= T <= %d drafted tokens", T, kMaxDrafts);
+  if (N < 0 || (long long)N + T > Ncap)
+    return fail(SK_ERR_INVALID_ARG, "N=%d cached and T=%d drafted keys do not fit Ncap=%d", N, T, Ncap);
+  SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_TREE_DECODE, B, Hq, Hkv, Ncap, N, d, 0, T)));
+  CacheAttendParams p = cache_params(Q, K, V, scales, lens, Hq, Hkv, Ncap, N);
+  p.mode = KEYS_TREE;
+  p.T = T;
+  p.mask = reinterpret_cast<const uint32_t*>(mask);
+  p.mask_words = (T + 31) / 32;
+  p.n = N + T;
+  return attend(p, q, kv, B, d, scale, O, o, ws, false, as_stream(stream));
+}
+
+}  // extern "C"

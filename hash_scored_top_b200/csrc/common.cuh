@@ -13,11 +13,12 @@ constexpr unsigned FULL = 0xffffffffu;
 // ---------------------------------------------------------------- error word
 // Set by a kernel that has to give up (a bounded wait that ran out, a
 // shared-memory plan that does not fit) -- never by a trap. Read and cleared by
-// sk_check_status on the host. The library is a single translation unit.
-__device__ unsigned int g_error_word = 0u;
+// sk_check_status on the host. Each translation unit has its own.
+static __device__ unsigned int g_error_word = 0u;
 constexpr unsigned ERR_TIMEOUT = 1u;   // a bounded wait gave up
 constexpr unsigned ERR_LAYOUT = 2u;    // a launch's shared-memory plan did not fit
 constexpr unsigned ERR_RANGE = 4u;     // a page-table entry outside the pool (read as page 0)
+constexpr unsigned ERR_ROWS = 8u;      // a row to write lay outside the cache (not written)
 
 // ---------------------------------------------------------------- bucket-ID cache layout
 // Each key stores its L bucket IDs in LP bytes, split in chunks of S_0, S_1

@@ -59,7 +59,9 @@
 extern "C" {
 #endif
 
-typedef enum { SK_F32 = 0, SK_BF16 = 1 } sk_dtype;
+/* SK_INT8 and SK_E4M3 are storage of a quantised cache only: the entry points
+ * that take such a cache say so, every other rejects them. */
+typedef enum { SK_F32 = 0, SK_BF16 = 1, SK_INT8 = 2, SK_E4M3 = 3 } sk_dtype;
 
 typedef enum {
   SK_OK = 0,
@@ -86,7 +88,14 @@ typedef enum {
   SK_OP_DECODE_ADAPTIVE = 11,        /* k is k_max */
   SK_OP_DECODE_ADAPTIVE_HEADS = 12,  /* k is k_max */
   SK_OP_SPARSE_ATTEND_PAGED = 13,
-  SK_OP_DECODE_PAGED = 14
+  SK_OP_DECODE_PAGED = 14,
+  SK_OP_QUANT_DECODE = 15,
+  SK_OP_QUANT_SPARSE_ATTEND = 16,
+  SK_OP_SOCKET_DECODE_QUANT = 17,
+  SK_OP_BLOCK_SELECT = 18,           /* L is the block size, k the blocks kept */
+  SK_OP_BLOCK_ATTEND = 19,           /* as SK_OP_BLOCK_SELECT */
+  SK_OP_BLOCK_DECODE = 20,           /* as SK_OP_BLOCK_SELECT */
+  SK_OP_TREE_DECODE = 21             /* k is T, the drafted tokens */
 } sk_op;
 
 /*
@@ -379,6 +388,145 @@ int dense_decode(const void* Q, const void* K, const void* V, sk_dtype kv, int B
 int socket_soft_count_attend(const void* Q, const void* V, sk_dtype kv, const void* R, const void* ids, const int* idx,
                              int B, int Hq, int Hkv, int Ncap, int d, int L, int P, float tau, int k, float* O,
                              void* ws, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Quantised caches, block selection, drafted tokens
+ * ----------------------------------------------------------------------
+ * These operators have no counterpart in the pages; they are the cache formats
+ * and decode steps that a serving loop puts around the ones above.
+ *
+ * Quantised cache: Kq, Vq [B][Hkv][Ncap][d] bytes (SK_INT8 or SK_E4M3) and
+ * scales [B][Hkv][Ncap][2] f32, the K row's scale and the V row's: a value is
+ * code * scale. Of a row with largest magnitude a,
+ *   SK_INT8  scale = max(a / 127, 2^-126) rounded to f32, code = the integer
+ *            nearest x / scale (ties to even), in [-127, 127];
+ *   SK_E4M3  scale = 2^e, e the smallest integer >= -126 with a <= 448 * 2^e,
+ *            code = x / scale rounded to e4m3.
+ * A row of zeros has scale 0 and codes 0; a row with an infinity or a NaN has
+ * scale NaN and codes 0, and reads back as NaN.
+ *
+ * "Cache of any format" below: K and V f32 or bf16 (`scales` NULL, Q of the
+ * same type) or quantised (Q f32 or bf16).
+ *
+ * lens (nullable): [B] int32 device array, the keys in use of each sequence,
+ * clamped to [0, N]; NULL: N keys each. A sequence's keys at and behind its
+ * length are not read, whatever lies there. A query row that sees no key (or
+ * whose logits are all -infinity) gets 0.
+ * starts (nullable): [B] int32 device array, the first row of each sequence
+ * that the call works on, instead of n_begin. Rows [start, start + n_count) of
+ * a sequence are worked on as far as they lie in [0, Ncap) and, if lens is
+ * given, below lens[b]; the other rows of the cache (and of the outputs) stay as
+ * they are.
+ * O is f32 unless said otherwise, its layout as Q's. G = Hq / Hkv <= 8 and
+ * B * Hkv <= 65535 in all of them. ws must be 16-byte aligned.
+ */
+
+/*
+ * Quantises new rows as they are written to the cache: K_new, V_new (dtype
+ * src) hold row i of sequence b and KV head h at element b * stride_b +
+ * h * stride_h + i * stride_n (the d values of a row are contiguous; strides
+ * are multiples of 16 bytes, the same for K_new and V_new), i < n_count. It
+ * goes to cache row start + i. A row that falls outside [0, Ncap) though lens
+ * does not leave it out is not written and is reported by sk_check_status
+ * (SK_ERR_INVALID_ARG). Without starts, [n_begin, n_begin + n_count) must lie
+ * in [0, Ncap). n_count == 0 is a no-op.
+ */
+int quant_append(const void* K_new, const void* V_new, sk_dtype src, long long stride_b, long long stride_h,
+                 long long stride_n, const int* starts, const int* lens, int B, int Hkv, int Ncap, int n_begin,
+                 int n_count, int d, void* Kq, void* Vq, sk_dtype kv, float* scales, void* stream);
+
+/*
+ * Reads rows of a quantised cache back: K, V [B][Hkv][n_count][d] (dtype dst)
+ * get code * scale of cache rows start + i, rounded to f32 and then to dst.
+ */
+int quant_read(const void* Kq, const void* Vq, sk_dtype kv, const float* scales, const int* starts, const int* lens,
+               int B, int Hkv, int Ncap, int n_begin, int n_count, int d, void* K, void* V, sk_dtype dst, void* stream);
+
+/*
+ * dense_decode over a quantised cache: O_h = softmax(q_h . K^T * scale) V over
+ * the sequence's keys. Q [B][Hq][d]. ws: sk_workspace_bytes(SK_OP_QUANT_DECODE).
+ */
+int quant_decode(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                 const int* lens, int B, int Hq, int Hkv, int Ncap, int N, int d, float scale, float* O, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/*
+ * socket_sparse_attend over a quantised cache: attention over the rows
+ * idx[p][0 .. k) of each pair. Entries outside [0, Ncap) are left out (a list
+ * shorter than k is filled up with -1); a row that is listed twice counts
+ * twice. ws: sk_workspace_bytes(SK_OP_QUANT_SPARSE_ATTEND).
+ */
+int quant_sparse_attend(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                        const int* idx, int B, int Hq, int Hkv, int Ncap, int d, int k, float scale, float* O, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * The decode step of socket_decode with a quantised K/V cache: its selection
+ * (steps 2-4, from ids and norms), then quant_sparse_attend over it. idx_out
+ * (nullable): [B][Hkv][k]. ws: sk_workspace_bytes(SK_OP_SOCKET_DECODE_QUANT).
+ */
+int socket_decode_quant(const void* Q, sk_dtype q, const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
+                        const void* R, const void* ids, const void* norms, int B, int Hq, int Hkv, int Ncap, int N,
+                        int d, int L, int P, float tau, int k, float scale, float* O, int* idx_out, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * Block summaries: block j of a pair is its rows j * block .. j * block +
+ * block - 1 (block 16, 32, 64 or 128); bsum [B][Hkv][ceil(Ncap / block)][2][d]
+ * bf16 holds, per channel, the minimum and the maximum of the block's keys,
+ * rounded down and up. Recomputes every block that holds one of the rows
+ * [start, end), end = min(start + n_count, lens[b], Ncap), over its rows below
+ * end: after a prompt n_begin = 0, n_count = its length; after an appended
+ * token its row. K: cache of any format (scales as there). NaN keys are passed
+ * over.
+ */
+int block_summarize(const void* K, sk_dtype kv, const float* scales, const int* starts, const int* lens, int B, int Hkv,
+                    int Ncap, int n_begin, int n_count, int d, int block, void* bsum, void* stream);
+
+/*
+ * Chooses k blocks of each pair: the score of a block is
+ *   sum over the group's query heads h of sum_c max(q_hc min_c, q_hc max_c),
+ * the sum of the upper bounds on q_h . k that its summary gives, rounded once
+ * to f32. The sequence's first n_first and last n_last blocks (the last may be
+ * partly filled) are always in; the others by score, ties to the lower block,
+ * a NaN score below all. idx [B][Hkv][k] int32: ascending, and -1 where a
+ * sequence has fewer than k blocks. Q [B][Hq][d]. Requires n_first + n_last <=
+ * k. ws: sk_workspace_bytes(SK_OP_BLOCK_SELECT).
+ */
+int block_select(const void* Q, sk_dtype q, const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N,
+                 int d, int block, int k, int n_first, int n_last, int* idx, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention over the keys of the listed blocks idx [B][Hkv][k] (as far as they
+ * lie below the sequence's length; entries that are negative or behind the last
+ * block are left out; a block that is listed twice counts twice). Cache of any
+ * format. ws: sk_workspace_bytes(SK_OP_BLOCK_ATTEND).
+ */
+int block_attend(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                 const int* lens, const int* idx, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k,
+                 float scale, float* O, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * block_select, then block_attend over its choice. idx_out (nullable) receives
+ * the blocks. ws: sk_workspace_bytes(SK_OP_BLOCK_DECODE).
+ */
+int block_decode(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                 const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k,
+                 int n_first, int n_last, float scale, float* O, int* idx_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of T drafted tokens per sequence (1 <= T <= 256): Q [B][T][Hq][d].
+ * A sequence has lens[b] (or N) cached keys, which every token sees, and its
+ * drafted keys behind them: drafted key i is cache row lens[b] + i, seen by
+ * token t if bit i % 32 of mask[b][t][i / 32] is set (mask [B][T][ceil(T / 32)]
+ * int32). mask NULL: token t sees drafted keys 0 .. t (a chain). Bits past T are
+ * ignored. Requires 0 <= N, N + T <= Ncap. Cache of any format. O [B][T][Hq][d]
+ * of dtype o: SK_F32 is accurate to f32; with SK_BF16 the softmax weights may
+ * be rounded to 16 bits. ws: sk_workspace_bytes(SK_OP_TREE_DECODE).
+ */
+int tree_decode(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales,
+                const int* lens, const int* mask, int B, int T, int Hq, int Hkv, int Ncap, int N, int d, float scale,
+                void* O, sk_dtype o, void* ws, size_t ws_bytes, void* stream);
 
 /* Scratch bytes needed by `op` for these shapes (0 if none). Arguments an
  * op does not use are ignored. Returns (size_t)-1 for invalid shapes. */
