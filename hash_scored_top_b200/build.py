@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["csrc/api.cu", "csrc/cache_api.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17",
+    "-O3", "-lineinfo", "-std=c++20",
     "-Xcompiler", "-fPIC",
 ]
 

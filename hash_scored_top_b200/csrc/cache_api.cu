@@ -3,12 +3,14 @@
 // api.cu (everything is checked on the host before anything is launched,
 // nothing is allocated, all work is asynchronous on the caller's stream).
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "host.cuh"
 #include "blocks.cuh"
 #include "cache_attend.cuh"
 #include "quant.cuh"
+#include "stream_attend.cuh"
 
 using namespace hst;
 
@@ -18,9 +20,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // A kernel launch, as the programmatic dependent of the kernel before it on
 // the stream if `pdl` (it waits before it reads what that kernel writes).
-template <typename Params>
-int launch(void (*kern)(Params), dim3 grid, int threads, size_t smem, cudaStream_t s, bool pdl, const char* what,
-           const Params& p) {
+template <typename... Params>
+int launch(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool pdl, const char* what,
+           const std::type_identity_t<Params>&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
@@ -31,7 +33,7 @@ int launch(void (*kern)(Params), dim3 grid, int threads, size_t smem, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p...);
   if (e != cudaSuccess) return fail(SK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return check_launch(what);
 }
@@ -98,8 +100,55 @@ int rows_splits(int pairs, int R, int n) {
   return (int)std::max(1LL, std::min(want, (long long)(n + 63) / 64));
 }
 
+// Blocks of the stream kernel: one per SM, fewer when there are not enough
+// tiles to give each of their warps one.
+int stream_blocks(int pairs, int n) {
+  const long long tiles = (long long)pairs * ((n + 15) / 16);
+  return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + SA_WARPS - 1) / SA_WARPS));
+}
+
+// Workspace of the attention of R rows per pair: the larger of what its
+// kernels need (the query does not know the cache's format).
 size_t attend_bytes(int pairs, int R, int n, int d) {
-  return align256((size_t)pairs * R * rows_splits(pairs, R, n) * (d + 2) * sizeof(float));
+  const size_t rows = (size_t)pairs * R * rows_splits(pairs, R, n) * (d + 2) * sizeof(float);
+  const size_t stream = R <= 8 ? (size_t)(stream_blocks(pairs, n) + pairs) * R * (d + 2) * sizeof(float) : 0;
+  return align256(std::max(rows, stream));
+}
+
+// Allows a kernel its dynamic shared memory on the current device (once per
+// kernel and device; setting it twice does no harm).
+template <auto Kern>
+int allow_smem(size_t smem) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("cudaGetDevice");
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return SK_OK;
+  if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return check_launch("cudaFuncSetAttribute");
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return SK_OK;
+}
+
+template <int D, int FMT, bool QF32>
+int launch_stream(const StreamParams& sp, int B, int blocks, bool pdl, cudaStream_t s) {
+  SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32>>(StreamShape<D, FMT>::SMEM)));
+  return launch(stream_attend_kernel<D, FMT, QF32>, dim3(blocks), SA_THREADS, StreamShape<D, FMT>::SMEM, s, pdl,
+                "stream_attend_kernel", sp, B);
+}
+
+template <int D>
+int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, float* O, bool pdl, cudaStream_t s) {
+  StreamParams sp;
+  sp.a = p;
+  const int blocks = stream_blocks(B * p.Hkv, p.n);
+  const bool f = q == SK_F32;
+  SK_TRY(kv == SK_BF16   ? (launch_stream<D, KV_BF16, false>(sp, B, blocks, pdl, s))
+         : kv == SK_INT8 ? (f ? launch_stream<D, KV_INT8, true>(sp, B, blocks, pdl, s)
+                              : launch_stream<D, KV_INT8, false>(sp, B, blocks, pdl, s))
+                         : (f ? launch_stream<D, KV_E4M3, true>(sp, B, blocks, pdl, s)
+                              : launch_stream<D, KV_E4M3, false>(sp, B, blocks, pdl, s)));
+  return launch(stream_merge_kernel<D>, dim3(p.G, B * p.Hkv), 4 * D, 0, s, true, "stream_merge_kernel", sp, O, B, blocks);
 }
 
 template <int D>
@@ -120,6 +169,9 @@ int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float sca
   p.q_bf16 = q == SK_BF16;
   p.scale_log2 = scale * kLog2e;
   p.part = reinterpret_cast<float*>(ws);
+  if (kv != SK_F32 && p.mode != KEYS_TREE)
+    return d == 128 ? stream_attend<128>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s)
+                    : stream_attend<64>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s);
   p.splits = rows_splits(pairs, R, p.n);
   SK_TRY(d == 128 ? launch_rows<128>(p, kv, pairs, pdl, s) : launch_rows<64>(p, kv, pairs, pdl, s));
   CacheMergeParams m;

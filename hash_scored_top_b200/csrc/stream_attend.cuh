@@ -1,0 +1,537 @@
+// Attention of one token's G <= 8 query heads over a bf16 or 8-bit cache: all
+// keys of a sequence, listed rows, or listed blocks (see cache_attend.cuh).
+//
+// The kernel is bound by the cache's bytes: 4 D (bf16) or 2 D + 8 (8 bits) per
+// key and pair, against 4 D G flops. Everything follows from keeping those
+// bytes in flight and the work per byte small:
+//   * One persistent block per SM. The tiles of 16 positions of all pairs form
+//     one list, of which every block takes an equal run, whatever the lengths
+//     of the sequences are. A run that crosses a pair's end gives a partial
+//     (m, l, o[D]) per head for each side; stream_merge_kernel joins a pair's
+//     partials in order.
+//   * A tile is a warp's own work. Each lane copies (cp.async, 16 bytes) just
+//     the bytes that it will use itself to a slot of its own in shared memory
+//     and waits for its own copies only: no barriers, no bank conflicts, and
+//     the next tiles in flight cost no registers.
+//   * Tensor cores, m16n8k16. S[rows x keys] = Q . K^T has the heads in rows
+//     0..7 of M; rows 8..15 carry the low parts of an f32 query. S's
+//     accumulators are P's operand as they are: rows 0..7 its high parts, rows
+//     8..15 its low parts, so that one product per 8 columns of V gives both.
+//     The order of the head dimension inside S's products and of the columns
+//     of O is free, so a lane's 16 bytes of K are its operand, and its 16 bytes
+//     of four V rows are the four contraction rows of 16 (bf16: 8) columns.
+//   * 8-bit codes become f16 exactly. Queries are scaled by a power of two to
+//     fill f16 (an 11-bit high part holds a bf16 value; an f32 one takes two).
+//     A key's scale multiplies its logit, a value's scale its weight; weights
+//     are kept below 2^15 by a running power of two E, the largest exponent
+//     of a value scale so far, next to the running maximum, and enter as two
+//     f16 terms (22 bits). bf16 caches use bf16 products, weights in three
+//     terms (24 bits).
+#pragma once
+
+#include "cache_attend.cuh"
+
+namespace hst {
+
+constexpr int SA_WARPS = 12;
+constexpr int SA_THREADS = 32 * SA_WARPS;
+
+template <int D, int FMT>
+struct StreamShape {
+  static constexpr bool B16 = FMT == KV_BF16;
+  static constexpr int KC = (B16 ? 2 * D : D) / 64;       // 16-byte chunks of a K row per lane (4 lanes a row)
+  static constexpr int VB = (B16 ? 2 * D : D) / 8;        // bytes of a V row per lane (8 lanes a row): 32, 16 or 8
+  static constexpr int VC = VB >= 16 ? 4 * (VB / 16) : 2; // chunks of the lane's four V rows
+  static constexpr int SC = B16 ? 0 : 2;                  // chunks of the lane's four keys' scales
+  static constexpr int CHUNKS = 2 * KC + VC + SC;
+  static constexpr int STAGE = CHUNKS * 512;              // bytes per warp and stage
+  // as many stages as fit: bf16 D = 128 2 x 8 KB, D = 64 4 x 4 KB, 8 bits 3 x 5 KB and 4 x 3 KB, times 12 warps
+  static constexpr int STAGES = STAGE >= 8192 ? 2 : STAGE >= 5120 ? 3 : 4;
+  static constexpr int SMEM = SA_WARPS * STAGES * STAGE;
+  static_assert(STAGES * STAGE >= 8 * (D + 2) * 4, "a warp's partial lies in its own stages");
+};
+
+struct StreamParams {
+  CacheAttendParams a;
+};
+
+// Tiles of a sequence's pairs.
+__device__ __forceinline__ int stream_tiles(const CacheAttendParams& a, int b) {
+  if (a.mode == KEYS_ALL) return (seq_len(a.lens, b, a.N) + 15) / 16;
+  return (a.n + 15) / 16;
+}
+// Tiles of all pairs; with lengths of their own the sequences differ.
+__device__ __forceinline__ long long stream_total(const CacheAttendParams& a, int B) {
+  if (a.mode != KEYS_ALL || a.lens == nullptr) return (long long)B * a.Hkv * stream_tiles(a, 0);
+  long long t = 0;
+  for (int b = 0; b < B; ++b) t += (long long)a.Hkv * stream_tiles(a, b);
+  return t;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Copies 16 (8) bytes, or zeros where `on` is false (nothing is read then).
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void async_copy8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// Two f16 from the low (HI = false) or high pair of a word of codes. int8: the
+// code plus 128 in the mantissa of 1024.., less 1152; exact.
+template <int FMT, bool HI>
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t w) {
+  if constexpr (FMT == KV_INT8) {
+    const uint32_t m = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(HI ? w >> 16 : w & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  }
+}
+
+// 2^e as f32, |e| <= 126 (anything outside: the nearest of those).
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23); }
+
+template <int D, int FMT, bool QF32>
+__global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const StreamParams sp, int B) {
+  using SH = StreamShape<D, FMT>;
+  constexpr bool B16 = SH::B16;
+  constexpr int KS = D / 16, NT = D / 8;                   // steps of Q.K, column tiles of O
+  constexpr int KC = SH::KC, STAGES = SH::STAGES;
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  __shared__ float sm_w[SA_WARPS][8];                      // a warp's factor in the block's partial
+  __shared__ float sm_m[8], sm_l[8];
+  const CacheAttendParams& a = sp.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+  const int G = a.G;
+  const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * STAGES * SH::STAGE);
+  const unsigned char* K8 = reinterpret_cast<const unsigned char*>(a.K);
+  const unsigned char* V8 = reinterpret_cast<const unsigned char*>(a.V);
+  constexpr int ROW = B16 ? 2 * D : D;                     // bytes of a cache row
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // idx may be the previous kernel's
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this block's run of the list of tiles
+  const long long total = stream_total(a, B);
+  long long t0 = (long long)blockIdx.x * total / gridDim.x;
+  const long long t1 = (long long)(blockIdx.x + 1) * total / gridDim.x;
+  int b = 0;
+  long long first = 0;                                     // first tile of sequence b's pairs
+  while (t0 < t1) {
+    while (t0 >= first + (long long)a.Hkv * stream_tiles(a, b)) {
+      first += (long long)a.Hkv * stream_tiles(a, b);
+      ++b;
+    }
+    const int per = stream_tiles(a, b);
+    const int h = (int)((t0 - first) / per), pair = b * a.Hkv + h;
+    const int ta = (int)(t0 - first - (long long)h * per);
+    const int te = (int)min((long long)per, ta + (t1 - t0));
+    const int len = seq_len(a.lens, b, a.N);
+    const size_t base = (size_t)pair * a.Ncap;
+
+    // ---- the query rows as operands: word s of a lane covers dimensions dim(s) .. dim(s) + 3
+    uint32_t qh[KS][2], ql[QF32 ? KS : 1][2];
+    float qscale = a.scale_log2;
+    {
+      const size_t q0 = ((size_t)b * a.Hq + h * G + r) * D;
+      float4 q[KS];
+      float mx = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int dim = B16 ? 32 * (s >> 1) + 8 * c + 4 * (s & 1) : 64 * (s >> 2) + 16 * c + 4 * (s & 3);
+        q[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < G) {
+          if constexpr (QF32) q[s] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.Q) + q0 + dim);
+          else q[s] = row_quad<KV_BF16>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + q0, 0, D, dim / 4);
+        }
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(q[s].x), fabsf(q[s].y)), fmaxf(fabsf(q[s].z), fabsf(q[s].w))));
+      }
+      if constexpr (B16) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          qh[s][0] = pack_bf16x2(q[s].x, q[s].y);
+          qh[s][1] = pack_bf16x2(q[s].z, q[s].w);
+        }
+      } else {
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+        const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -112);     // 2^(13 - e) stays a number
+        const float f = pow2i(13 - e);
+        // two factors: their product may leave f32 where each does not
+        qscale = a.scale_log2 * pow2i((e - 13) / 2) * pow2i((e - 13) - (e - 13) / 2);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const float x = q[s].x * f, y = q[s].y * f, z = q[s].z * f, w = q[s].w * f;
+          qh[s][0] = pack_f16x2(x, y);
+          qh[s][1] = pack_f16x2(z, w);
+          if constexpr (QF32) {
+            const float2 lo = __half22float2(*reinterpret_cast<__half2*>(&qh[s][0]));
+            const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&qh[s][1]));
+            ql[s][0] = pack_f16x2(x - lo.x, y - lo.y);
+            ql[s][1] = pack_f16x2(z - hi.x, w - hi.y);
+          }
+        }
+      }
+    }
+
+    // ---- this warp's tiles ta + warp, ta + warp + SA_WARPS, ...
+    float acc[NT][4], m = -INFINITY, l = 0.f;
+    int E = -127;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+
+    // cache row of position 16 t + (lane & 15), or -1; t < te
+    auto row_at = [&](int t) -> int {
+      if (t >= te) return -1;
+      const int j = 16 * t + (lane & 15);
+      if (a.mode == KEYS_ALL) return j < len ? j : -1;
+      if (j >= a.n) return -1;
+      return key_row(a, pair, b, 0, len, j);
+    };
+    uint64_t seen = 0;                                     // 16 bits per tile in flight, newest lowest
+    int next_row = row_at(ta + warp);
+    int issued = ta + warp;                                // next tile to copy
+    auto issue = [&](int stage) {
+      const int row = next_row;
+      seen = (seen << 16) | (uint64_t)(__ballot_sync(FULL, row >= 0) & 0xffffu);
+      issued += SA_WARPS;
+      next_row = row_at(issued);                           // its latency passes behind this tile's copies
+      const uint32_t dst = ring + (uint32_t)(stage * SH::STAGE) + 16u * lane;
+      int q = 0;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int kr = __shfl_sync(FULL, row, r + 8 * n);
+        const unsigned char* src = K8 + (base + (size_t)max(kr, 0)) * ROW + 16 * c;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * q++, src + 64 * i, kr >= 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int vr = __shfl_sync(FULL, row, 2 * c + (i & 1) + 8 * (i >> 1));
+        const size_t at = base + (size_t)max(vr, 0);
+        const unsigned char* src = V8 + at * ROW;
+        if constexpr (SH::VB == 8) {
+          async_copy8(dst + 512u * (q + (i >> 1)) + 8u * (i & 1), src + 8 * r, vr >= 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < SH::VB / 16; ++k)
+            async_copy16(dst + 512u * (q + i * (SH::VB / 16) + k), src + 128 * k + 16 * r, vr >= 0);
+        }
+        if constexpr (!B16) async_copy8(dst + 512u * (q + SH::VC + (i >> 1)) + 8u * (i & 1), a.scales + 2 * at, vr >= 0);
+      }
+    };
+    const int mine = te - ta > warp ? (te - ta - warp + SA_WARPS - 1) / SA_WARPS : 0;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      if (s < mine) issue(s);
+      else seen <<= 16;
+      async_commit();
+    }
+    int stage = 0;
+    for (int i = 0; i < mine; ++i) {
+      {
+        const int ahead = stage == 0 ? STAGES - 1 : stage - 1;
+        if (i + STAGES - 1 < mine) issue(ahead);
+        else seen <<= 16;
+        async_commit();
+      }
+      async_wait<STAGES - 1>();
+      const uint32_t src = ring + (uint32_t)(stage * SH::STAGE) + 16u * lane;
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+      const uint32_t live = (uint32_t)(seen >> (16 * (STAGES - 1))) & 0xffffu;
+
+      // ---- S = Q . K^T, keys 8 n + (column) of the tile
+      float S[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        S[n][0] = S[n][1] = S[n][2] = S[n][3] = 0.f;
+#pragma unroll
+        for (int i2 = 0; i2 < KC; ++i2) {
+          const uint4 v = lds128(src + 512u * (n * KC + i2));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if constexpr (B16) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              mma_bf16_16816(S[n], qh[2 * i2 + u][0], 0u, qh[2 * i2 + u][1], 0u, w[2 * u], w[2 * u + 1]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int s = 4 * i2 + u;
+              mma_f16_16816(S[n], qh[s][0], QF32 ? ql[QF32 ? s : 0][0] : 0u, qh[s][1], QF32 ? ql[QF32 ? s : 0][1] : 0u,
+                            codes_to_f16x2<FMT, false>(w[u]), codes_to_f16x2<FMT, true>(w[u]));
+            }
+          }
+        }
+      }
+
+      // ---- weights of head r for keys 2c, 2c + 1, 2c + 8, 2c + 9
+      float s[4] = {S[0][0] + S[0][2], S[0][1] + S[0][3], S[1][0] + S[1][2], S[1][1] + S[1][3]};
+      float vs[4] = {1.f, 1.f, 1.f, 1.f};
+      int e = E;
+      if constexpr (!B16) {
+        const uint4 x = lds128(src + 512u * (2 * KC + SH::VC)), y = lds128(src + 512u * (2 * KC + SH::VC + 1));
+        const float ks[4] = {__uint_as_float(x.x), __uint_as_float(x.z), __uint_as_float(y.x), __uint_as_float(y.z)};
+        vs[0] = __uint_as_float(x.y);
+        vs[1] = __uint_as_float(x.w);
+        vs[2] = __uint_as_float(y.y);
+        vs[3] = __uint_as_float(y.w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] *= ks[k];
+        float vm = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+        vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, 1));
+        vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, 2));
+        if (vm < INFINITY) e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);      // not a NaN either
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = (live >> (2 * c + (k & 1) + 8 * (k >> 1))) & 1u ? s[k] * qscale : -INFINITY;
+      float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 2));
+      if (__any_sync(FULL, mt > m || e > E)) {             // rare once the maximum has settled
+        const float mn = fmaxf(m, mt);
+        float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        m = mn;
+        l *= f;
+        f *= exp2f((float)(E - e));
+        E = e;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[j][0] *= f;
+          acc[j][1] *= f;
+          acc[j][2] *= f;
+          acc[j][3] *= f;
+        }
+      }
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = s[k] == -INFINITY ? 0.f : exp2f(s[k] - m);
+        l += w[k];
+      }
+      uint32_t pa[4], pl[2] = {0u, 0u};                    // operand: rows 0..7 high, rows 8..15 low parts
+      if constexpr (B16) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t hi = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+          const float x = w[2 * k] - bf16lo_to_f32(hi), y = w[2 * k + 1] - bf16hi_to_f32(hi);
+          const uint32_t mid = pack_bf16x2(x, y);
+          pa[2 * k] = hi;
+          pa[2 * k + 1] = mid;
+          pl[k] = pack_bf16x2(x - bf16lo_to_f32(mid), y - bf16hi_to_f32(mid));
+        }
+      } else {
+        const int e1 = E >> 1;
+        const float f1 = pow2i(-e1), f2 = pow2i(13 - (E - e1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] *= (vs[k] * f1) * f2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          pa[2 * k] = pack_f16x2(w[2 * k], w[2 * k + 1]);
+          const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * k]));
+          pa[2 * k + 1] = pack_f16x2(w[2 * k] - hi.x, w[2 * k + 1] - hi.y);
+        }
+      }
+
+      // ---- O += P . V, column tile by column tile
+      if constexpr (B16) {
+#pragma unroll
+        for (int k = 0; k < SH::VB / 16; ++k) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            const uint4 x = lds128(src + 512u * (2 * KC + i2 * (SH::VB / 16) + k));
+            v[i2][0] = x.x;
+            v[i2][1] = x.y;
+            v[i2][2] = x.z;
+            v[i2][3] = x.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int sel = j & 1 ? 0x7632 : 0x5410;
+            const uint32_t b0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
+            mma_bf16_16816(acc[8 * k + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
+            mma_bf16_16816(acc[8 * k + j], pl[0], 0u, pl[1], 0u, b0, b1);
+          }
+        }
+      } else {
+        uint32_t v[4][SH::VB / 4];
+        if constexpr (SH::VB == 16) {
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            const uint4 x = lds128(src + 512u * (2 * KC + i2));
+            v[i2][0] = x.x;
+            v[i2][1] = x.y;
+            v[i2][2] = x.z;
+            v[i2][3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            const uint4 x = lds128(src + 512u * (2 * KC + i2));
+            v[2 * i2][0] = x.x;
+            v[2 * i2][1] = x.y;
+            v[2 * i2 + 1][0] = x.z;
+            v[2 * i2 + 1][1] = x.w;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < SH::VB / 4; ++q) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {                    // columns 4 q + 2 u, 4 q + 2 u + 1
+            const int sel = u ? 0x7362 : 0x5140;
+            const uint32_t x = __byte_perm(v[0][q], v[1][q], sel), y = __byte_perm(v[2][q], v[3][q], sel);
+            mma_f16_16816(acc[4 * q + 2 * u], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, false>(x),
+                          codes_to_f16x2<FMT, false>(y));
+            mma_f16_16816(acc[4 * q + 2 * u + 1], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, true>(x),
+                          codes_to_f16x2<FMT, true>(y));
+          }
+        }
+      }
+    }
+    async_wait<0>();
+
+    // ---- the block's partial: every warp's (m, l, o) into its own stages, joined in warp order
+    l += __shfl_xor_sync(FULL, l, 1);
+    l += __shfl_xor_sync(FULL, l, 2);
+    float* mine_s = reinterpret_cast<float*>(dyn + (size_t)warp * STAGES * SH::STAGE);
+    __syncwarp();                                          // other lanes' slots of the ring are done with
+    if (r < G) {
+      if (c == 0) {
+        mine_s[r] = m;
+        mine_s[8 + r] = l;
+      }
+      const int e1 = E >> 1;
+      const float f1 = B16 ? 1.f : pow2i(e1 - 13), f2 = B16 ? 1.f : pow2i(E - e1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int n = 2 * c + k;                         // the lane row whose column this is
+          const int col = B16 ? 64 * (j >> 3) + 8 * n + (j & 7) : SH::VB * n + j;
+          mine_s[16 + r * D + col] = (acc[j][k] + acc[j][2 + k]) * f1 * f2;
+        }
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 8 && threadIdx.x < G) {
+      const int g = threadIdx.x;
+      float mm = -INFINITY, ls = 0.f;
+      for (int w = 0; w < SA_WARPS; ++w)
+        mm = fmaxf(mm, reinterpret_cast<float*>(dyn + (size_t)w * STAGES * SH::STAGE)[g]);
+      for (int w = 0; w < SA_WARPS; ++w) {
+        const float* p = reinterpret_cast<float*>(dyn + (size_t)w * STAGES * SH::STAGE);
+        const float f = mm == -INFINITY ? 1.f : exp2f(p[g] - mm);
+        sm_w[w][g] = f;
+        ls = fmaf(f, p[8 + g], ls);
+      }
+      sm_m[g] = mm;
+      sm_l[g] = ls;
+    }
+    __syncthreads();
+    float* out = a.part + ((size_t)blockIdx.x + pair) * G * (D + 2);
+    for (int x = threadIdx.x; x < G * D; x += SA_THREADS) {
+      const int g = x / D, col = x % D;
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < SA_WARPS; ++w)
+        o = fmaf(sm_w[w][g], reinterpret_cast<float*>(dyn + (size_t)w * STAGES * SH::STAGE)[16 + x], o);
+      out[g * (D + 2) + 2 + col] = o;
+    }
+    if (threadIdx.x < G) {
+      out[threadIdx.x * (D + 2)] = sm_m[threadIdx.x];
+      out[threadIdx.x * (D + 2) + 1] = sm_l[threadIdx.x];
+    }
+    t0 += te - ta;
+    __syncthreads();                                       // the stages are free for the next pair
+  }
+}
+
+// Joins a pair's partials (those of blocks i0 .. i1, in order). grid = (G, pairs); 4 groups of D threads take a quarter
+// of the partials each.
+template <int D>
+__global__ void __launch_bounds__(4 * D) stream_merge_kernel(const StreamParams sp, float* O, int B, int blocks) {
+  __shared__ float sm[4], sl[4], so[4][D];
+  const CacheAttendParams& a = sp.a;
+  const int g = blockIdx.x, pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
+  const int col = threadIdx.x % D, grp = threadIdx.x / D;
+  long long first = 0, total = 0;
+  const int per = stream_tiles(a, b);
+  if (a.mode != KEYS_ALL || a.lens == nullptr) {
+    total = (long long)B * a.Hkv * per;
+    first = (long long)pair * per;
+  } else {
+    for (int i = 0; i < B; ++i) {
+      const long long t = (long long)a.Hkv * stream_tiles(a, i);
+      if (i < b) first += t;
+      total += t;
+    }
+    first += (long long)h * per;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float* out = O + ((size_t)b * a.Hq + h * a.G + g) * D;
+  if (per == 0) {                                          // no keys
+    if (grp == 0) out[col] = 0.f;
+    return;
+  }
+  // block i holds tile x if floor(i T / n) <= x < floor((i + 1) T / n)
+  const int i0 = (int)(((first + 1) * blocks - 1) / total), i1 = (int)(((first + per) * blocks - 1) / total);
+  const float* part = a.part + (size_t)g * (D + 2);
+  const size_t step = (size_t)a.G * (D + 2);
+  float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int i = i0 + grp; i <= i1; i += 4) {
+    const float* p = part + (size_t)(i + pair) * step;
+    const float pm = __ldcg(p), pl = __ldcg(p + 1), po = __ldcg(p + 2 + col);
+    const float mn = fmaxf(m, pm);
+    const float f0 = mn == -INFINITY ? 1.f : exp2f(m - mn), f1 = mn == -INFINITY ? 1.f : exp2f(pm - mn);
+    m = mn;
+    l = fmaf(f1, pl, l * f0);
+    o = fmaf(f1, po, o * f0);
+  }
+  if (col == 0) {
+    sm[grp] = m;
+    sl[grp] = l;
+  }
+  so[grp][col] = o;
+  __syncthreads();
+  if (grp > 0) return;
+  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  l = o = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = mm == -INFINITY ? 1.f : exp2f(sm[k] - mm);
+    l = fmaf(f, sl[k], l);
+    o = fmaf(f, so[k][col], o);
+  }
+  out[col] = l == 0.f ? 0.f : o / l;
+}
+
+}  // namespace hst
