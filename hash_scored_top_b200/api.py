@@ -511,19 +511,30 @@ def _cache_code(t: torch.Tensor, quantised: bool = False) -> int:
     return code
 
 
-def _on(first: torch.Tensor, *others):
-    """The device's guard: every tensor lies on `first`'s CUDA device, which the call makes current."""
-    dev = first.device
-    if dev.type != "cuda":
+def _device(first: torch.Tensor, *others) -> int:
+    """Index of the CUDA device that every tensor given lies on."""
+    i = first.get_device()
+    if i < 0:
         raise ValueError("tensors must live on a CUDA device")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
-    return torch.cuda.device(dev)
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device expected")
+    return i
+
+
+def _run(device: int, what: str, fn, *args):
+    """fn(*args, the device's current stream) with that device current; raises the library's message."""
+    if device == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if rc != 0:
+        _check(rc, what)
 
 
 def _addr(t):
-    """Address of a contiguous tensor (its device was checked by _on), or None."""
+    """Address of a contiguous tensor (its device was checked by _device), or None."""
     if t is None:
         return None
     if not t.is_contiguous():
@@ -531,16 +542,15 @@ def _addr(t):
     return t.data_ptr()
 
 
-def _want_cache(K, V, scales):
+def _want_cache(K, V, scales, quantised: bool = False):
     """Checks K, V and their scales; returns the cache's dtype code."""
-    code = _cache_code(K)
-    B, Hkv, Ncap, d = K.shape
-    if V is not None:
+    code = _cache_code(K, quantised)
+    if V is not None and (V.dtype != K.dtype or V.shape != K.shape):
         _want(V, K.dtype, K.shape, "V")
     if code >= SK_INT8:
         if scales is None:
             raise ValueError("scales: a quantised cache needs them")
-        _want(scales, torch.float32, (B, Hkv, Ncap, 2), "scales")
+        _want(scales, torch.float32, (*K.shape[:3], 2), "scales")
     elif scales is not None:
         raise ValueError(f"scales: a {K.dtype} cache has none")
     return code
@@ -549,10 +559,6 @@ def _want_cache(K, V, scales):
 def _want_lens(lens, B, name="lens"):
     if lens is not None:
         _want(lens, torch.int32, (B,), name)
-
-
-def _raw_stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ws_arg(ws, op, device, *shape):
@@ -567,8 +573,7 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     (or starts[b] ..) of a quantised cache (see the C header)."""
     B, Hkv, Ncap, d = Kq.shape
     n = K_new.shape[2]
-    _cache_code(Kq, quantised=True)
-    code = _want_cache(Kq, Vq, scales)
+    code = _want_cache(Kq, Vq, scales, quantised=True)
     _want(K_new, K_new.dtype, (B, Hkv, n, d), "K_new")
     _want(V_new, K_new.dtype, (B, Hkv, n, d), "V_new")
     _want_lens(starts, B, "starts")
@@ -578,42 +583,37 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     sb, sh, sn, sd = K_new.stride()
     if sd != 1:
         raise ValueError("K_new, V_new: the last dimension must be contiguous")
-    with _on(Kq, Vq, scales, K_new, V_new, starts, lens):
-        rc = _lib.lib.quant_append(K_new.data_ptr(), V_new.data_ptr(), _dtype_code(K_new), sb, sh, sn, _addr(starts), _addr(lens),
-                                   B, Hkv, Ncap, n_begin, n, d, _addr(Kq), _addr(Vq), code, _addr(scales), _raw_stream(Kq))
-    _check(rc, "quant_append")
+    i = _device(Kq, Vq, scales, K_new, V_new, starts, lens)
+    _run(i, "quant_append", _lib.lib.quant_append, K_new.data_ptr(), V_new.data_ptr(), _dtype_code(K_new), sb, sh, sn,
+         _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n, d, _addr(Kq), _addr(Vq), code, _addr(scales))
 
 
 def quant_read(Kq, Vq, scales, K, V, n_begin: int = 0, starts=None, lens=None):
     """Reads rows n_begin .. (or starts[b] ..) of a quantised cache back into K, V [B, Hkv, n, d] (f32 or bf16)."""
     B, Hkv, Ncap, d = Kq.shape
     n = K.shape[2]
-    _cache_code(Kq, quantised=True)
-    code = _want_cache(Kq, Vq, scales)
+    code = _want_cache(Kq, Vq, scales, quantised=True)
     _want(K, K.dtype, (B, Hkv, n, d), "K")
     _want(V, K.dtype, (B, Hkv, n, d), "V")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
-    with _on(Kq, Vq, scales, K, V, starts, lens):
-        rc = _lib.lib.quant_read(_addr(Kq), _addr(Vq), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n,
-                                 d, _addr(K), _addr(V), _dtype_code(K), _raw_stream(Kq))
-    _check(rc, "quant_read")
+    i = _device(Kq, Vq, scales, K, V, starts, lens)
+    _run(i, "quant_read", _lib.lib.quant_read, _addr(Kq), _addr(Vq), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv,
+         Ncap, n_begin, n, d, _addr(K), _addr(V), _dtype_code(K))
 
 
 def quant_decode(Q, Kq, Vq, scales, N: int, scale: float, O, lens=None, ws=None):
     """Dense decode attention over a quantised cache: O [B, Hq, d] f32 (see the C header)."""
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
-    _cache_code(Kq, quantised=True)
-    code = _want_cache(Kq, Vq, scales)
+    code = _want_cache(Kq, Vq, scales, quantised=True)
     _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
     _want(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
-    with _on(Q, Kq, Vq, scales, O, lens, ws):
-        ws, w, wb = _ws_arg(ws, OP_QUANT_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d)
-        rc = _lib.lib.quant_decode(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(lens), B, Hq, Hkv,
-                                   Ncap, N, d, scale, _addr(O), w, wb, _raw_stream(Q))
-    _check(rc, "quant_decode")
+    i = _device(Q, Kq, Vq, scales, O, lens, ws)
+    ws, w, wb = _ws_arg(ws, OP_QUANT_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d)
+    _run(i, "quant_decode", _lib.lib.quant_decode, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales),
+         _addr(lens), B, Hq, Hkv, Ncap, N, d, scale, _addr(O), w, wb)
 
 
 def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
@@ -621,16 +621,14 @@ def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
     k = idx.shape[-1]
-    _cache_code(Kq, quantised=True)
-    code = _want_cache(Kq, Vq, scales)
+    code = _want_cache(Kq, Vq, scales, quantised=True)
     _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
     _want(idx, torch.int32, (B, Hkv, k), "idx")
     _want(O, torch.float32, (B, Hq, d), "O")
-    with _on(Q, Kq, Vq, scales, idx, O, ws):
-        ws, w, wb = _ws_arg(ws, OP_QUANT_SPARSE_ATTEND, Q.device, B, Hq, Hkv, Ncap, k, d, 0, 0, k)
-        rc = _lib.lib.quant_sparse_attend(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(idx), B, Hq,
-                                          Hkv, Ncap, d, k, scale, _addr(O), w, wb, _raw_stream(Q))
-    _check(rc, "quant_sparse_attend")
+    i = _device(Q, Kq, Vq, scales, idx, O, ws)
+    ws, w, wb = _ws_arg(ws, OP_QUANT_SPARSE_ATTEND, Q.device, B, Hq, Hkv, Ncap, k, d, 0, 0, k)
+    _run(i, "quant_sparse_attend", _lib.lib.quant_sparse_attend, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code,
+         _addr(scales), _addr(idx), B, Hq, Hkv, Ncap, d, k, scale, _addr(O), w, wb)
 
 
 def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int, tau: float, k: int, scale: float, O,
@@ -638,8 +636,7 @@ def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int
     """socket_decode over a quantised K/V cache (the hashed-key cache as there): O [B, Hq, d] f32."""
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
-    _cache_code(Kq, quantised=True)
-    code = _want_cache(Kq, Vq, scales)
+    code = _want_cache(Kq, Vq, scales, quantised=True)
     _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
     _want(R, torch.bfloat16, (L * P, d), "R")
     _want(ids, torch.uint8, (B, Hkv, Ncap, ids_bytes_per_key(L)), "ids")
@@ -647,12 +644,11 @@ def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int
     _want(O, torch.float32, (B, Hq, d), "O")
     if idx_out is not None:
         _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
-    with _on(Q, Kq, Vq, scales, R, ids, norms, O, idx_out, ws):
-        ws, w, wb = _ws_arg(ws, OP_SOCKET_DECODE_QUANT, Q.device, B, Hq, Hkv, Ncap, N, d, L, P, k)
-        rc = _lib.lib.socket_decode_quant(_addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales), _addr(R), _addr(ids),
-                                          _addr(norms), B, Hq, Hkv, Ncap, N, d, L, P, tau, k, scale, _addr(O), _addr(idx_out), w,
-                                          wb, _raw_stream(Q))
-    _check(rc, "socket_decode_quant")
+    i = _device(Q, Kq, Vq, scales, R, ids, norms, O, idx_out, ws)
+    ws, w, wb = _ws_arg(ws, OP_SOCKET_DECODE_QUANT, Q.device, B, Hq, Hkv, Ncap, N, d, L, P, k)
+    _run(i, "socket_decode_quant", _lib.lib.socket_decode_quant, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code,
+         _addr(scales), _addr(R), _addr(ids), _addr(norms), B, Hq, Hkv, Ncap, N, d, L, P, tau, k, scale, _addr(O),
+         _addr(idx_out), w, wb)
 
 
 def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None = None, scales=None, starts=None, lens=None):
@@ -663,10 +659,9 @@ def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None =
     _want(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
-    with _on(K, scales, bsum, starts, lens):
-        rc = _lib.lib.block_summarize(_addr(K), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n_count, d,
-                                      block, _addr(bsum), _raw_stream(K))
-    _check(rc, "block_summarize")
+    i = _device(K, scales, bsum, starts, lens)
+    _run(i, "block_summarize", _lib.lib.block_summarize, _addr(K), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv,
+         Ncap, n_begin, n_count, d, block, _addr(bsum))
 
 
 def _block_shapes(Q, bsum, Ncap, block):
@@ -682,11 +677,10 @@ def block_select(Q, bsum, Ncap: int, N: int, block: int, n_first: int, n_last: i
     k = idx.shape[-1]
     _want(idx, torch.int32, (B, Hkv, k), "idx")
     _want_lens(lens, B)
-    with _on(Q, bsum, idx, lens, ws):
-        ws, w, wb = _ws_arg(ws, OP_BLOCK_SELECT, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-        rc = _lib.lib.block_select(_addr(Q), _dtype_code(Q), _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d, block, k, n_first,
-                                   n_last, _addr(idx), w, wb, _raw_stream(Q))
-    _check(rc, "block_select")
+    i = _device(Q, bsum, idx, lens, ws)
+    ws, w, wb = _ws_arg(ws, OP_BLOCK_SELECT, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    _run(i, "block_select", _lib.lib.block_select, _addr(Q), _dtype_code(Q), _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d,
+         block, k, n_first, n_last, _addr(idx), w, wb)
 
 
 def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None, lens=None, ws=None):
@@ -699,11 +693,10 @@ def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None,
     _want(idx, torch.int32, (B, Hkv, k), "idx")
     _want(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
-    with _on(Q, K, V, scales, idx, O, lens, ws):
-        ws, w, wb = _ws_arg(ws, OP_BLOCK_ATTEND, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-        rc = _lib.lib.block_attend(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(lens), _addr(idx), B,
-                                   Hq, Hkv, Ncap, N, d, block, k, scale, _addr(O), w, wb, _raw_stream(Q))
-    _check(rc, "block_attend")
+    i = _device(Q, K, V, scales, idx, O, lens, ws)
+    ws, w, wb = _ws_arg(ws, OP_BLOCK_ATTEND, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    _run(i, "block_attend", _lib.lib.block_attend, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
+         _addr(lens), _addr(idx), B, Hq, Hkv, Ncap, N, d, block, k, scale, _addr(O), w, wb)
 
 
 def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last: int, scale: float, O, scales=None, lens=None,
@@ -717,12 +710,10 @@ def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last
     if idx_out is not None:
         _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
     _want_lens(lens, B)
-    with _on(Q, K, V, scales, bsum, O, lens, idx_out, ws):
-        ws, w, wb = _ws_arg(ws, OP_BLOCK_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-        rc = _lib.lib.block_decode(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(bsum), _addr(lens), B,
-                                   Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, scale, _addr(O), _addr(idx_out), w, wb,
-                                   _raw_stream(Q))
-    _check(rc, "block_decode")
+    i = _device(Q, K, V, scales, bsum, O, lens, idx_out, ws)
+    ws, w, wb = _ws_arg(ws, OP_BLOCK_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    _run(i, "block_decode", _lib.lib.block_decode, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
+         _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, scale, _addr(O), _addr(idx_out), w, wb)
 
 
 def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=None, ws=None):
@@ -736,8 +727,7 @@ def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=N
     if mask is not None:
         _want(mask, torch.int32, (B, T, -(-T // 32)), "mask")
     _want_lens(lens, B)
-    with _on(Q, K, V, scales, O, mask, lens, ws):
-        ws, w, wb = _ws_arg(ws, OP_TREE_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, 0, 0, T)
-        rc = _lib.lib.tree_decode(_addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales), _addr(lens), _addr(mask), B, T,
-                                  Hq, Hkv, Ncap, N, d, scale, _addr(O), _dtype_code(O), w, wb, _raw_stream(Q))
-    _check(rc, "tree_decode")
+    i = _device(Q, K, V, scales, O, mask, lens, ws)
+    ws, w, wb = _ws_arg(ws, OP_TREE_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, 0, 0, T)
+    _run(i, "tree_decode", _lib.lib.tree_decode, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
+         _addr(lens), _addr(mask), B, T, Hq, Hkv, Ncap, N, d, scale, _addr(O), _dtype_code(O), w, wb)

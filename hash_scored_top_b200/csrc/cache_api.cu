@@ -51,7 +51,7 @@ int check_formats(sk_dtype q, sk_dtype kv, const float* scales) {
   SK_TRY(check_dtype(q));
   if (is_8bit(kv)) {
     SK_NONNULL(scales);
-    SK_ALIGNED(scales, 8);
+    SK_ALIGNED(scales, 16);
     return SK_OK;
   }
   SK_TRY(check_dtype(kv));
@@ -103,7 +103,7 @@ int rows_splits(int pairs, int R, int n) {
 // Blocks of the stream kernel: one per SM, fewer when there are not enough
 // tiles to give each of their warps one.
 int stream_blocks(int pairs, int n) {
-  const long long tiles = (long long)pairs * ((n + 15) / 16);
+  const long long tiles = (long long)pairs * ((n + 31) / 32);
   return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + SA_WARPS - 1) / SA_WARPS));
 }
 
@@ -131,24 +131,32 @@ int allow_smem(size_t smem) {
 }
 
 template <int D, int FMT, bool QF32>
-int launch_stream(const StreamParams& sp, int B, int blocks, bool pdl, cudaStream_t s) {
-  SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32>>(StreamShape<D, FMT>::SMEM)));
-  return launch(stream_attend_kernel<D, FMT, QF32>, dim3(blocks), SA_THREADS, StreamShape<D, FMT>::SMEM, s, pdl,
-                "stream_attend_kernel", sp, B);
+int launch_stream(const CacheAttendParams& p, int B, float* O, bool pdl, cudaStream_t s) {
+  using SH = StreamShape<D, FMT>;
+  StreamParams sp;
+  sp.a = p;
+  const int blocks = stream_blocks(B * p.Hkv, p.n);
+  // listed rows are those of a quantised cache: bf16 caches have socket_sparse_attend
+  constexpr bool CAN_LIST = FMT != KV_BF16;
+  if (CAN_LIST && p.mode == KEYS_LISTED) {
+    SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32, CAN_LIST>>(SH::SMEM)));
+    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, CAN_LIST>, dim3(blocks), SA_THREADS, SH::SMEM, s, pdl,
+                  "stream_attend_kernel", sp, B));
+  } else {
+    SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32, false>>(SH::SMEM)));
+    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, false>, dim3(blocks), SA_THREADS, SH::SMEM, s, pdl,
+                  "stream_attend_kernel", sp, B));
+  }
+  return launch(stream_merge_kernel<D, SH::TILE>, dim3(p.G, B * p.Hkv), 4 * D, 0, s, true, "stream_merge_kernel", sp, O, B,
+                blocks);
 }
 
 template <int D>
 int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, float* O, bool pdl, cudaStream_t s) {
-  StreamParams sp;
-  sp.a = p;
-  const int blocks = stream_blocks(B * p.Hkv, p.n);
   const bool f = q == SK_F32;
-  SK_TRY(kv == SK_BF16   ? (launch_stream<D, KV_BF16, false>(sp, B, blocks, pdl, s))
-         : kv == SK_INT8 ? (f ? launch_stream<D, KV_INT8, true>(sp, B, blocks, pdl, s)
-                              : launch_stream<D, KV_INT8, false>(sp, B, blocks, pdl, s))
-                         : (f ? launch_stream<D, KV_E4M3, true>(sp, B, blocks, pdl, s)
-                              : launch_stream<D, KV_E4M3, false>(sp, B, blocks, pdl, s)));
-  return launch(stream_merge_kernel<D>, dim3(p.G, B * p.Hkv), 4 * D, 0, s, true, "stream_merge_kernel", sp, O, B, blocks);
+  return kv == SK_BF16   ? launch_stream<D, KV_BF16, false>(p, B, O, pdl, s)
+         : kv == SK_INT8 ? (f ? launch_stream<D, KV_INT8, true>(p, B, O, pdl, s) : launch_stream<D, KV_INT8, false>(p, B, O, pdl, s))
+                         : (f ? launch_stream<D, KV_E4M3, true>(p, B, O, pdl, s) : launch_stream<D, KV_E4M3, false>(p, B, O, pdl, s));
 }
 
 template <int D>
@@ -166,6 +174,8 @@ int launch_rows(const CacheAttendParams& p, sk_dtype kv, int pairs, bool pdl, cu
 int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float scale, void* O, sk_dtype o, void* ws,
            bool pdl, cudaStream_t s) {
   const int pairs = B * p.Hkv, R = p.T * p.G;
+  if ((long long)pairs * ((p.n + 15LL) / 16) > INT_MAX)
+    return fail(SK_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of 16 keys");
   p.q_bf16 = q == SK_BF16;
   p.scale_log2 = scale * kLog2e;
   p.part = reinterpret_cast<float*>(ws);
@@ -354,7 +364,7 @@ int quant_append(const void* K_new, const void* V_new, sk_dtype src, long long s
   SK_ALIGNED(V_new, 16);
   SK_ALIGNED(Kq, 16);
   SK_ALIGNED(Vq, 16);
-  SK_ALIGNED(scales, 8);
+  SK_ALIGNED(scales, 16);
   SK_TRY(check_dtype(src));
   SK_TRY(check_8bit(kv));
   SK_TRY(check_grid(B, Hkv, Hkv, d));
@@ -398,7 +408,7 @@ int quant_read(const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
   SK_NONNULL(V);
   SK_ALIGNED(Kq, 16);
   SK_ALIGNED(Vq, 16);
-  SK_ALIGNED(scales, 8);
+  SK_ALIGNED(scales, 16);
   SK_ALIGNED(K, 16);
   SK_ALIGNED(V, 16);
   SK_TRY(check_8bit(kv));

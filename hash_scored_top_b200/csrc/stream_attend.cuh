@@ -4,15 +4,16 @@
 // The kernel is bound by the cache's bytes: 4 D (bf16) or 2 D + 8 (8 bits) per
 // key and pair, against 4 D G flops. Everything follows from keeping those
 // bytes in flight and the work per byte small:
-//   * One persistent block per SM. The tiles of 16 positions of all pairs form
-//     one list, of which every block takes an equal run, whatever the lengths
-//     of the sequences are. A run that crosses a pair's end gives a partial
+//   * One persistent block per SM. The tiles of all pairs form one list, of
+//     which every block takes an equal run, whatever the lengths of the
+//     sequences are. A run that crosses a pair's end gives a partial
 //     (m, l, o[D]) per head for each side; stream_merge_kernel joins a pair's
 //     partials in order.
-//   * A tile is a warp's own work. Each lane copies (cp.async, 16 bytes) just
-//     the bytes that it will use itself to a slot of its own in shared memory
-//     and waits for its own copies only: no barriers, no bank conflicts, and
-//     the next tiles in flight cost no registers.
+//   * A tile (32 positions, 16 for bf16 with D = 128) is a warp's own work.
+//     Each lane copies (cp.async, 16 bytes) just the bytes of K and V that it
+//     will use itself to a slot of its own in shared memory: no barriers, no
+//     bank conflicts, and the next tile in flight costs no registers. Only the
+//     scales of a tile are shared by the lanes.
 //   * Tensor cores, m16n8k16. S[rows x keys] = Q . K^T has the heads in rows
 //     0..7 of M; rows 8..15 carry the low parts of an f32 query. S's
 //     accumulators are P's operand as they are: rows 0..7 its high parts, rows
@@ -23,7 +24,7 @@
 //   * 8-bit codes become f16 exactly. Queries are scaled by a power of two to
 //     fill f16 (an 11-bit high part holds a bf16 value; an f32 one takes two).
 //     A key's scale multiplies its logit, a value's scale its weight; weights
-//     are kept below 2^15 by a running power of two E, the largest exponent
+//     are kept below 2^15 by a running power of two, from the largest exponent
 //     of a value scale so far, next to the running maximum, and enter as two
 //     f16 terms (22 bits). bf16 caches use bf16 products, weights in three
 //     terms (24 bits).
@@ -36,19 +37,24 @@ namespace hst {
 constexpr int SA_WARPS = 12;
 constexpr int SA_THREADS = 32 * SA_WARPS;
 
+// A stage of a warp's ring: HALVES x 16 positions, each of CHUNKS x 512 bytes
+// (16 per lane) and the scales of its 16 rows.
 template <int D, int FMT>
 struct StreamShape {
   static constexpr bool B16 = FMT == KV_BF16;
-  static constexpr int KC = (B16 ? 2 * D : D) / 64;       // 16-byte chunks of a K row per lane (4 lanes a row)
-  static constexpr int VB = (B16 ? 2 * D : D) / 8;        // bytes of a V row per lane (8 lanes a row): 32, 16 or 8
+  static constexpr int ROW = B16 ? 2 * D : D;             // bytes of a cache row
+  static constexpr int KC = ROW / 64;                     // 16-byte chunks of a K row per lane (4 lanes a row)
+  static constexpr int VB = ROW / 8;                      // bytes of a V row per lane (8 lanes a row): 32, 16 or 8
   static constexpr int VC = VB >= 16 ? 4 * (VB / 16) : 2; // chunks of the lane's four V rows
-  static constexpr int SC = B16 ? 0 : 2;                  // chunks of the lane's four keys' scales
-  static constexpr int CHUNKS = 2 * KC + VC + SC;
-  static constexpr int STAGE = CHUNKS * 512;              // bytes per warp and stage
-  // as many stages as fit: bf16 D = 128 2 x 8 KB, D = 64 4 x 4 KB, 8 bits 3 x 5 KB and 4 x 3 KB, times 12 warps
-  static constexpr int STAGES = STAGE >= 8192 ? 2 : STAGE >= 5120 ? 3 : 4;
+  static constexpr int CHUNKS = 2 * KC + VC;
+  static constexpr int HALF = CHUNKS * 512 + (B16 ? 0 : 128);
+  static constexpr int HALVES = HALF > 8000 ? 1 : 2;
+  static constexpr int TILE = 16 * HALVES;                // positions
+  static constexpr int STAGE = HALVES * HALF;
+  // 12 warps x 2 stages of 8 KB, or 3 of the 4 KB of 8 bits and D = 64
+  static constexpr int STAGES = STAGE > 6000 ? 2 : 3;
   static constexpr int SMEM = SA_WARPS * STAGES * STAGE;
-  static_assert(STAGES * STAGE >= 8 * (D + 2) * 4, "a warp's partial lies in its own stages");
+  static_assert(STAGES * STAGE >= (8 * D + 16) * 4, "a warp's partial lies in its own stages");
 };
 
 struct StreamParams {
@@ -56,17 +62,36 @@ struct StreamParams {
 };
 
 // Tiles of a sequence's pairs.
+template <int TILE>
 __device__ __forceinline__ int stream_tiles(const CacheAttendParams& a, int b) {
-  if (a.mode == KEYS_ALL) return (seq_len(a.lens, b, a.N) + 15) / 16;
-  return (a.n + 15) / 16;
+  return ((a.mode == KEYS_ALL ? seq_len(a.lens, b, a.N) : a.n) + TILE - 1) / TILE;
 }
-// Tiles of all pairs; with lengths of their own the sequences differ.
-__device__ __forceinline__ long long stream_total(const CacheAttendParams& a, int B) {
-  if (a.mode != KEYS_ALL || a.lens == nullptr) return (long long)B * a.Hkv * stream_tiles(a, 0);
-  long long t = 0;
-  for (int b = 0; b < B; ++b) t += (long long)a.Hkv * stream_tiles(a, b);
-  return t;
-}
+
+// The list of all pairs' tiles (fewer than 2^31, checked on the host), cut into
+// one run per block: the first `rem` runs have one tile more than the others.
+struct StreamRuns {
+  int total, q, rem;
+  template <int TILE>
+  __device__ __forceinline__ static StreamRuns make(const CacheAttendParams& a, int B, int blocks) {
+    StreamRuns s;
+    if (a.mode != KEYS_ALL || a.lens == nullptr) {
+      s.total = B * a.Hkv * stream_tiles<TILE>(a, 0);
+    } else {
+      s.total = 0;
+      for (int b = 0; b < B; ++b) s.total += a.Hkv * stream_tiles<TILE>(a, b);
+    }
+    s.q = (int)((uint32_t)s.total / (uint32_t)blocks);
+    s.rem = s.total - s.q * blocks;
+    return s;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * q + min(i, rem); }
+  // the run that tile x lies in
+  __device__ __forceinline__ int of(int x) const {
+    const int cut = rem * (q + 1);
+    if (x < cut) return (int)((uint32_t)x / (uint32_t)(q + 1));
+    return rem + (int)((uint32_t)(x - cut) / (uint32_t)q);       // q > 0: there are tiles behind the cut
+  }
+};
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
@@ -81,12 +106,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Copies 16 (8) bytes, or zeros where `on` is false (nothing is read then).
-__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+// Copies `bytes` (0 to 16, or 8) and fills up with zeros; with 0 nothing is read.
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void async_copy8(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+__device__ __forceinline__ void async_copy8(uint32_t dst, const void* src, int bytes = 8) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -120,12 +145,19 @@ __device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t w) {
 // 2^e as f32, |e| <= 126 (anything outside: the nearest of those).
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23); }
 
-template <int D, int FMT, bool QF32>
+// 2^x, 2 units in the last place; 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, int FMT, bool QF32, bool LISTED>
 __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const StreamParams sp, int B) {
   using SH = StreamShape<D, FMT>;
   constexpr bool B16 = SH::B16;
   constexpr int KS = D / 16, NT = D / 8;                   // steps of Q.K, column tiles of O
-  constexpr int KC = SH::KC, STAGES = SH::STAGES;
+  constexpr int KC = SH::KC, STAGES = SH::STAGES, HALVES = SH::HALVES, ROW = SH::ROW, TILE = SH::TILE;
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ float sm_w[SA_WARPS][8];                      // a warp's factor in the block's partial
   __shared__ float sm_m[8], sm_l[8];
@@ -133,29 +165,162 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
   const int G = a.G;
   const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * STAGES * SH::STAGE);
-  const unsigned char* K8 = reinterpret_cast<const unsigned char*>(a.K);
-  const unsigned char* V8 = reinterpret_cast<const unsigned char*>(a.V);
-  constexpr int ROW = B16 ? 2 * D : D;                     // bytes of a cache row
   asm volatile("griddepcontrol.wait;" ::: "memory");       // idx may be the previous kernel's
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // this block's run of the list of tiles
-  const long long total = stream_total(a, B);
-  long long t0 = (long long)blockIdx.x * total / gridDim.x;
-  const long long t1 = (long long)(blockIdx.x + 1) * total / gridDim.x;
-  int b = 0;
-  long long first = 0;                                     // first tile of sequence b's pairs
+  const StreamRuns runs = StreamRuns::make<TILE>(a, B, gridDim.x);
+  int t0 = runs.begin(blockIdx.x);
+  const int t1 = runs.begin(blockIdx.x + 1);
+  int b = 0, first = 0;                                    // first tile of sequence b's pairs
   while (t0 < t1) {
-    while (t0 >= first + (long long)a.Hkv * stream_tiles(a, b)) {
-      first += (long long)a.Hkv * stream_tiles(a, b);
-      ++b;
+    int per;
+    for (;; ++b) {
+      per = stream_tiles<TILE>(a, b);
+      if (t0 - first < a.Hkv * per) break;
+      first += a.Hkv * per;
     }
-    const int per = stream_tiles(a, b);
-    const int h = (int)((t0 - first) / per), pair = b * a.Hkv + h;
-    const int ta = (int)(t0 - first - (long long)h * per);
-    const int te = (int)min((long long)per, ta + (t1 - t0));
+    const int h = (int)((uint32_t)(t0 - first) / (uint32_t)per), pair = b * a.Hkv + h;
+    const int ta = t0 - first - h * per;
+    const int te = min(per, ta + (t1 - t0));
     const int len = seq_len(a.lens, b, a.N);
     const size_t base = (size_t)pair * a.Ncap;
+    const unsigned char* Kp = reinterpret_cast<const unsigned char*>(a.K) + base * ROW + 16 * c;
+    const unsigned char* Vp = reinterpret_cast<const unsigned char*>(a.V) + base * ROW + (SH::VB >= 16 ? 16 : 8) * r;
+    const float* Sp = a.scales + 2 * base;
+
+    // ---- the copies of a tile. Listed: lane i holds position i's row. Else a half's 16 positions are 16 rows from
+    // `row` on, the first `cnt` of which are seen.
+    struct Half {
+      int row, cnt;
+    };
+    auto half_at = [&](int t, int hf) -> Half {
+      Half x = {0, 0};
+      const int j = TILE * t + 16 * hf;
+      if (t >= te || j >= a.n) return x;
+      x.row = j;
+      if (a.mode == KEYS_BLOCKS) {
+        const int bl = __ldg(a.idx + (size_t)pair * a.k + j / a.block);
+        if (bl < 0 || bl > (len - 1) / a.block) return x;
+        x.row = bl * a.block + j % a.block;
+      }
+      x.cnt = min(max(len - x.row, 0), 16);
+      if (x.cnt == 0) x.row = 0;
+      return x;
+    };
+    auto listed_at = [&](int t) -> int {
+      const int j = TILE * t + lane;
+      return t < te && lane < TILE && j < a.n ? key_row(a, pair, b, 0, len, j) : -1;
+    };
+    uint32_t seen[3] = {0u, 0u, 0u};                       // a bit per position of the tiles in flight, newest first
+    auto shift_in = [&](uint32_t bits) {
+      seen[2] = seen[1];
+      seen[1] = seen[0];
+      seen[0] = bits;
+    };
+    Half nx[HALVES];
+    int nl = -1;
+    int next = ta + warp;                                  // next tile to copy
+    auto look = [&](int t) {                               // a tile's rows, ahead of its copies
+      if constexpr (LISTED) {
+        nl = listed_at(t);
+      } else {
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) nx[hf] = half_at(t, hf);
+      }
+    };
+    auto issue = [&](int stage) {
+      uint32_t bits = 0u;
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf) {
+        const uint32_t dst = ring + (uint32_t)(stage * SH::STAGE + hf * SH::HALF) + 16u * lane;
+        const uint32_t sdst = ring + (uint32_t)(stage * SH::STAGE + hf * SH::HALF + SH::CHUNKS * 512);
+        if constexpr (LISTED) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int kr = __shfl_sync(FULL, nl, 16 * hf + r + 8 * n);
+            const unsigned char* src = Kp + (size_t)max(kr, 0) * ROW;
+#pragma unroll
+            for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * (n * KC + i), src + 64 * i, kr >= 0 ? 16 : 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int vr = __shfl_sync(FULL, nl, 16 * hf + 2 * c + (i & 1) + 8 * (i >> 1));
+            const unsigned char* src = Vp + (size_t)max(vr, 0) * ROW;
+            if constexpr (SH::VB == 8) {
+              async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src, vr >= 0 ? 8 : 0);
+            } else {
+#pragma unroll
+              for (int k = 0; k < SH::VB / 16; ++k)
+                async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + 128 * k, vr >= 0 ? 16 : 0);
+            }
+          }
+          if constexpr (!B16) {
+            const int sr = __shfl_sync(FULL, nl, 16 * hf + (lane & 15));
+            if (lane < 16) async_copy8(sdst + 8u * lane, Sp + 2 * (size_t)max(sr, 0), sr >= 0 ? 8 : 0);
+          }
+        } else {
+          const Half x = nx[hf];
+          bits |= ((1u << x.cnt) - 1u) << (16 * hf);
+          const unsigned char* ks = Kp + ((size_t)x.row + r) * ROW;
+          const unsigned char* vs = Vp + ((size_t)x.row + 2 * c) * ROW;
+          if (x.cnt == 16) {                               // the common case: constant offsets
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * (n * KC + i), ks + 8 * n * ROW + 64 * i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const unsigned char* src = vs + ((i & 1) + 8 * (i >> 1)) * ROW;
+              if constexpr (SH::VB == 8) {
+                async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src);
+              } else {
+#pragma unroll
+                for (int k = 0; k < SH::VB / 16; ++k)
+                  async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + 128 * k);
+              }
+            }
+            if constexpr (!B16)
+              if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + 2 * lane));
+          } else {                                         // rows past the end are not read: zeros
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < KC; ++i) {
+                const bool on = r + 8 * n < x.cnt;
+                async_copy16(dst + 512u * (n * KC + i), on ? ks + 8 * n * ROW + 64 * i : Kp, on ? 16 : 0);
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = (i & 1) + 8 * (i >> 1);
+              const bool on = 2 * c + j < x.cnt;
+              const unsigned char* src = on ? vs + j * ROW : Vp;
+              if constexpr (SH::VB == 8) {
+                async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src, on ? 8 : 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < SH::VB / 16; ++k)
+                  async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + (on ? 128 * k : 0), on ? 16 : 0);
+              }
+            }
+            if constexpr (!B16)
+              if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + min(2 * lane, 14)), min(max(8 * (x.cnt - 2 * lane), 0), 16));
+          }
+        }
+      }
+      if constexpr (LISTED) bits = __ballot_sync(FULL, nl >= 0);
+      shift_in(bits);
+      next += SA_WARPS;
+      look(next);
+    };
+    const int mine = te - ta > warp ? (te - ta - warp + SA_WARPS - 1) / SA_WARPS : 0;
+    look(next);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      if (s < mine) issue(s);
+      else shift_in(0u);
+      async_commit();
+    }
 
     // ---- the query rows as operands: word s of a lane covers dimensions dim(s) .. dim(s) + 3
     uint32_t qh[KS][2], ql[QF32 ? KS : 1][2];
@@ -205,77 +370,33 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
     // ---- this warp's tiles ta + warp, ta + warp + SA_WARPS, ...
     float acc[NT][4], m = -INFINITY, l = 0.f;
     int E = -127;
+    float vf = pow2i(13 - E);                              // weights' factor
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-
-    // cache row of position 16 t + (lane & 15), or -1; t < te
-    auto row_at = [&](int t) -> int {
-      if (t >= te) return -1;
-      const int j = 16 * t + (lane & 15);
-      if (a.mode == KEYS_ALL) return j < len ? j : -1;
-      if (j >= a.n) return -1;
-      return key_row(a, pair, b, 0, len, j);
-    };
-    uint64_t seen = 0;                                     // 16 bits per tile in flight, newest lowest
-    int next_row = row_at(ta + warp);
-    int issued = ta + warp;                                // next tile to copy
-    auto issue = [&](int stage) {
-      const int row = next_row;
-      seen = (seen << 16) | (uint64_t)(__ballot_sync(FULL, row >= 0) & 0xffffu);
-      issued += SA_WARPS;
-      next_row = row_at(issued);                           // its latency passes behind this tile's copies
-      const uint32_t dst = ring + (uint32_t)(stage * SH::STAGE) + 16u * lane;
-      int q = 0;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int kr = __shfl_sync(FULL, row, r + 8 * n);
-        const unsigned char* src = K8 + (base + (size_t)max(kr, 0)) * ROW + 16 * c;
-#pragma unroll
-        for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * q++, src + 64 * i, kr >= 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int vr = __shfl_sync(FULL, row, 2 * c + (i & 1) + 8 * (i >> 1));
-        const size_t at = base + (size_t)max(vr, 0);
-        const unsigned char* src = V8 + at * ROW;
-        if constexpr (SH::VB == 8) {
-          async_copy8(dst + 512u * (q + (i >> 1)) + 8u * (i & 1), src + 8 * r, vr >= 0);
-        } else {
-#pragma unroll
-          for (int k = 0; k < SH::VB / 16; ++k)
-            async_copy16(dst + 512u * (q + i * (SH::VB / 16) + k), src + 128 * k + 16 * r, vr >= 0);
-        }
-        if constexpr (!B16) async_copy8(dst + 512u * (q + SH::VC + (i >> 1)) + 8u * (i & 1), a.scales + 2 * at, vr >= 0);
-      }
-    };
-    const int mine = te - ta > warp ? (te - ta - warp + SA_WARPS - 1) / SA_WARPS : 0;
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      if (s < mine) issue(s);
-      else seen <<= 16;
-      async_commit();
-    }
     int stage = 0;
     for (int i = 0; i < mine; ++i) {
       {
         const int ahead = stage == 0 ? STAGES - 1 : stage - 1;
         if (i + STAGES - 1 < mine) issue(ahead);
-        else seen <<= 16;
+        else shift_in(0u);
         async_commit();
       }
       async_wait<STAGES - 1>();
+      if constexpr (!B16) __syncwarp();                    // the scales were copied by other lanes
       const uint32_t src = ring + (uint32_t)(stage * SH::STAGE) + 16u * lane;
+      const uint32_t ssrc = ring + (uint32_t)(stage * SH::STAGE + SH::CHUNKS * 512) + 16u * c;
       stage = stage == STAGES - 1 ? 0 : stage + 1;
-      const uint32_t live = (uint32_t)(seen >> (16 * (STAGES - 1))) & 0xffffu;
+      const uint32_t live = seen[STAGES - 1];
 
-      // ---- S = Q . K^T, keys 8 n + (column) of the tile
-      float S[2][4];
+      // ---- S = Q . K^T: n counts groups of 8 keys
+      float S[2 * HALVES][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        S[n][0] = S[n][1] = S[n][2] = S[n][3] = 0.f;
+      for (int n = 0; n < 2 * HALVES; ++n) S[n][0] = S[n][1] = S[n][2] = S[n][3] = 0.f;
 #pragma unroll
-        for (int i2 = 0; i2 < KC; ++i2) {
-          const uint4 v = lds128(src + 512u * (n * KC + i2));
+      for (int i2 = 0; i2 < KC; ++i2) {
+#pragma unroll
+        for (int n = 0; n < 2 * HALVES; ++n) {
+          const uint4 v = lds128(src + (uint32_t)((n >> 1) * SH::HALF) + 512u * ((n & 1) * KC + i2));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if constexpr (B16) {
 #pragma unroll
@@ -292,36 +413,54 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
         }
       }
 
-      // ---- weights of head r for keys 2c, 2c + 1, 2c + 8, 2c + 9
-      float s[4] = {S[0][0] + S[0][2], S[0][1] + S[0][3], S[1][0] + S[1][2], S[1][1] + S[1][3]};
-      float vs[4] = {1.f, 1.f, 1.f, 1.f};
+      // ---- weights of head r for the keys 2c, 2c + 1 of each group
+      constexpr int NW = 4 * HALVES;
+      float s[NW], vs[B16 ? 1 : NW];
       int e = E;
-      if constexpr (!B16) {
-        const uint4 x = lds128(src + 512u * (2 * KC + SH::VC)), y = lds128(src + 512u * (2 * KC + SH::VC + 1));
-        const float ks[4] = {__uint_as_float(x.x), __uint_as_float(x.z), __uint_as_float(y.x), __uint_as_float(y.z)};
-        vs[0] = __uint_as_float(x.y);
-        vs[1] = __uint_as_float(x.w);
-        vs[2] = __uint_as_float(y.y);
-        vs[3] = __uint_as_float(y.w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] *= ks[k];
-        float vm = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+      for (int n = 0; n < 2 * HALVES; ++n) {
+        s[2 * n] = QF32 ? S[n][0] + S[n][2] : S[n][0];
+        s[2 * n + 1] = QF32 ? S[n][1] + S[n][3] : S[n][1];
+      }
+      if constexpr (!B16) {
+        float vm = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2 * HALVES; ++n) {             // (scale of K, scale of V) of two rows
+          const uint4 x = lds128(ssrc + (uint32_t)((n >> 1) * SH::HALF) + 64u * (n & 1));
+          s[2 * n] *= __uint_as_float(x.x);
+          s[2 * n + 1] *= __uint_as_float(x.z);
+          vs[2 * n] = __uint_as_float(x.y);
+          vs[2 * n + 1] = __uint_as_float(x.w);
+          vm = fmaxf(vm, fmaxf(fabsf(vs[2 * n]), fabsf(vs[2 * n + 1])));
+        }
         vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, 1));
         vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, 2));
         if (vm < INFINITY) e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);      // not a NaN either
       }
+      float mt = -INFINITY;
+      if (live == (TILE == 32 ? 0xffffffffu : 0xffffu)) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] = (live >> (2 * c + (k & 1) + 8 * (k >> 1))) & 1u ? s[k] * qscale : -INFINITY;
-      float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+        for (int k = 0; k < NW; ++k) s[k] *= qscale;
+      } else {
+        const uint32_t my = live >> (2 * c);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) s[k] = (my >> ((k & 1) + 8 * (k >> 1))) & 1u ? s[k] * qscale : -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < NW; ++k) mt = fmaxf(mt, s[k]);
       mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 1));
       mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, 2));
       if (__any_sync(FULL, mt > m || e > E)) {             // rare once the maximum has settled
         const float mn = fmaxf(m, mt);
-        float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        float f = mn == -INFINITY ? 1.f : ex2(m - mn);
         m = mn;
         l *= f;
-        f *= exp2f((float)(E - e));
-        E = e;
+        if constexpr (!B16) {
+          const float nf = pow2i(13 - e);
+          f *= nf / vf;                                    // a power of two
+          vf = nf;
+          E = e;
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           acc[j][0] *= f;
@@ -330,91 +469,92 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
           acc[j][3] *= f;
         }
       }
-      float w[4];
+      const float ms = m == -INFINITY ? 0.f : m;           // no finite logit yet: all weights are 0
+      float w[NW];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[k] = s[k] == -INFINITY ? 0.f : exp2f(s[k] - m);
+      for (int k = 0; k < NW; ++k) {
+        w[k] = ex2(s[k] - ms);
         l += w[k];
-      }
-      uint32_t pa[4], pl[2] = {0u, 0u};                    // operand: rows 0..7 high, rows 8..15 low parts
-      if constexpr (B16) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t hi = pack_bf16x2(w[2 * k], w[2 * k + 1]);
-          const float x = w[2 * k] - bf16lo_to_f32(hi), y = w[2 * k + 1] - bf16hi_to_f32(hi);
-          const uint32_t mid = pack_bf16x2(x, y);
-          pa[2 * k] = hi;
-          pa[2 * k + 1] = mid;
-          pl[k] = pack_bf16x2(x - bf16lo_to_f32(mid), y - bf16hi_to_f32(mid));
-        }
-      } else {
-        const int e1 = E >> 1;
-        const float f1 = pow2i(-e1), f2 = pow2i(13 - (E - e1));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] *= (vs[k] * f1) * f2;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          pa[2 * k] = pack_f16x2(w[2 * k], w[2 * k + 1]);
-          const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * k]));
-          pa[2 * k + 1] = pack_f16x2(w[2 * k] - hi.x, w[2 * k + 1] - hi.y);
-        }
+        if constexpr (!B16) w[k] *= vs[k] * vf;
       }
 
-      // ---- O += P . V, column tile by column tile
-      if constexpr (B16) {
+      // ---- O += P . V, half by half, column tile by column tile
 #pragma unroll
-        for (int k = 0; k < SH::VB / 16; ++k) {
-          uint32_t v[4][4];
+      for (int hf = 0; hf < HALVES; ++hf) {
+        const uint32_t vsrc = src + (uint32_t)(hf * SH::HALF) + 512u * (2 * KC);
+        uint32_t pa[4], pl[2] = {0u, 0u};                  // operand: rows 0..7 high, rows 8..15 low parts
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            const uint4 x = lds128(src + 512u * (2 * KC + i2 * (SH::VB / 16) + k));
-            v[i2][0] = x.x;
-            v[i2][1] = x.y;
-            v[i2][2] = x.z;
-            v[i2][3] = x.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int sel = j & 1 ? 0x7632 : 0x5410;
-            const uint32_t b0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
-            mma_bf16_16816(acc[8 * k + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
-            mma_bf16_16816(acc[8 * k + j], pl[0], 0u, pl[1], 0u, b0, b1);
+        for (int k = 0; k < 2; ++k) {
+          const float x = w[4 * hf + 2 * k], y = w[4 * hf + 2 * k + 1];
+          if constexpr (B16) {
+            const uint32_t hi = pack_bf16x2(x, y);
+            const float x1 = x - bf16lo_to_f32(hi), y1 = y - bf16hi_to_f32(hi);
+            const uint32_t mid = pack_bf16x2(x1, y1);
+            pa[2 * k] = hi;
+            pa[2 * k + 1] = mid;
+            pl[k] = pack_bf16x2(x1 - bf16lo_to_f32(mid), y1 - bf16hi_to_f32(mid));
+          } else {
+            pa[2 * k] = pack_f16x2(x, y);
+            const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * k]));
+            pa[2 * k + 1] = pack_f16x2(x - hi.x, y - hi.y);
           }
         }
-      } else {
-        uint32_t v[4][SH::VB / 4];
-        if constexpr (SH::VB == 16) {
+        if constexpr (B16) {
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            const uint4 x = lds128(src + 512u * (2 * KC + i2));
-            v[i2][0] = x.x;
-            v[i2][1] = x.y;
-            v[i2][2] = x.z;
-            v[i2][3] = x.w;
+          for (int k = 0; k < SH::VB / 16; ++k) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int i2 = 0; i2 < 4; ++i2) {
+              const uint4 x = lds128(vsrc + 512u * (i2 * (SH::VB / 16) + k));
+              v[i2][0] = x.x;
+              v[i2][1] = x.y;
+              v[i2][2] = x.z;
+              v[i2][3] = x.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int sel = j & 1 ? 0x7632 : 0x5410;
+              const uint32_t b0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
+              mma_bf16_16816(acc[8 * k + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
+              mma_bf16_16816(acc[8 * k + j], pl[0], 0u, pl[1], 0u, b0, b1);
+            }
           }
         } else {
+          uint32_t v[4][SH::VB / 4];
+          if constexpr (SH::VB == 16) {
 #pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            const uint4 x = lds128(src + 512u * (2 * KC + i2));
-            v[2 * i2][0] = x.x;
-            v[2 * i2][1] = x.y;
-            v[2 * i2 + 1][0] = x.z;
-            v[2 * i2 + 1][1] = x.w;
+            for (int i2 = 0; i2 < 4; ++i2) {
+              const uint4 x = lds128(vsrc + 512u * i2);
+              v[i2][0] = x.x;
+              v[i2][1] = x.y;
+              v[i2][2] = x.z;
+              v[i2][3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              const uint4 x = lds128(vsrc + 512u * i2);
+              v[2 * i2][0] = x.x;
+              v[2 * i2][1] = x.y;
+              v[2 * i2 + 1][0] = x.z;
+              v[2 * i2 + 1][1] = x.w;
+            }
           }
-        }
 #pragma unroll
-        for (int q = 0; q < SH::VB / 4; ++q) {
+          for (int q = 0; q < SH::VB / 4; ++q) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {                    // columns 4 q + 2 u, 4 q + 2 u + 1
-            const int sel = u ? 0x7362 : 0x5140;
-            const uint32_t x = __byte_perm(v[0][q], v[1][q], sel), y = __byte_perm(v[2][q], v[3][q], sel);
-            mma_f16_16816(acc[4 * q + 2 * u], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, false>(x),
-                          codes_to_f16x2<FMT, false>(y));
-            mma_f16_16816(acc[4 * q + 2 * u + 1], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, true>(x),
-                          codes_to_f16x2<FMT, true>(y));
+            for (int u = 0; u < 2; ++u) {                  // columns 4 q + 2 u, 4 q + 2 u + 1
+              const int sel = u ? 0x7362 : 0x5140;
+              const uint32_t x = __byte_perm(v[0][q], v[1][q], sel), y = __byte_perm(v[2][q], v[3][q], sel);
+              mma_f16_16816(acc[4 * q + 2 * u], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, false>(x),
+                            codes_to_f16x2<FMT, false>(y));
+              mma_f16_16816(acc[4 * q + 2 * u + 1], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, true>(x),
+                            codes_to_f16x2<FMT, true>(y));
+            }
           }
         }
       }
+      if constexpr (!B16) __syncwarp();                    // every lane has read the scales: they may be overwritten
     }
     async_wait<0>();
 
@@ -428,15 +568,14 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
         mine_s[r] = m;
         mine_s[8 + r] = l;
       }
-      const int e1 = E >> 1;
-      const float f1 = B16 ? 1.f : pow2i(e1 - 13), f2 = B16 ? 1.f : pow2i(E - e1);
+      const float of = B16 ? 1.f : 1.f / vf;               // a power of two
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int n = 2 * c + k;                         // the lane row whose column this is
           const int col = B16 ? 64 * (j >> 3) + 8 * n + (j & 7) : SH::VB * n + j;
-          mine_s[16 + r * D + col] = (acc[j][k] + acc[j][2 + k]) * f1 * f2;
+          mine_s[16 + r * D + col] = (acc[j][k] + acc[j][2 + k]) * of;
         }
       }
     }
@@ -444,11 +583,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
     if (threadIdx.x < 8 && threadIdx.x < G) {
       const int g = threadIdx.x;
       float mm = -INFINITY, ls = 0.f;
+#pragma unroll
       for (int w = 0; w < SA_WARPS; ++w)
         mm = fmaxf(mm, reinterpret_cast<float*>(dyn + (size_t)w * STAGES * SH::STAGE)[g]);
+#pragma unroll
       for (int w = 0; w < SA_WARPS; ++w) {
         const float* p = reinterpret_cast<float*>(dyn + (size_t)w * STAGES * SH::STAGE);
-        const float f = mm == -INFINITY ? 1.f : exp2f(p[g] - mm);
+        const float f = mm == -INFINITY ? 1.f : ex2(p[g] - mm);
         sm_w[w][g] = f;
         ls = fmaf(f, p[8 + g], ls);
       }
@@ -476,24 +617,18 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
 
 // Joins a pair's partials (those of blocks i0 .. i1, in order). grid = (G, pairs); 4 groups of D threads take a quarter
 // of the partials each.
-template <int D>
+template <int D, int TILE>
 __global__ void __launch_bounds__(4 * D) stream_merge_kernel(const StreamParams sp, float* O, int B, int blocks) {
   __shared__ float sm[4], sl[4], so[4][D];
   const CacheAttendParams& a = sp.a;
   const int g = blockIdx.x, pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
   const int col = threadIdx.x % D, grp = threadIdx.x / D;
-  long long first = 0, total = 0;
-  const int per = stream_tiles(a, b);
-  if (a.mode != KEYS_ALL || a.lens == nullptr) {
-    total = (long long)B * a.Hkv * per;
-    first = (long long)pair * per;
-  } else {
-    for (int i = 0; i < B; ++i) {
-      const long long t = (long long)a.Hkv * stream_tiles(a, i);
-      if (i < b) first += t;
-      total += t;
-    }
-    first += (long long)h * per;
+  const int per = stream_tiles<TILE>(a, b);
+  const StreamRuns runs = StreamRuns::make<TILE>(a, B, blocks);
+  int first = pair * per;                                  // the pair's first tile
+  if (a.mode == KEYS_ALL && a.lens != nullptr) {
+    first = h * per;
+    for (int i = 0; i < b; ++i) first += a.Hkv * stream_tiles<TILE>(a, i);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float* out = O + ((size_t)b * a.Hq + h * a.G + g) * D;
@@ -501,8 +636,7 @@ __global__ void __launch_bounds__(4 * D) stream_merge_kernel(const StreamParams 
     if (grp == 0) out[col] = 0.f;
     return;
   }
-  // block i holds tile x if floor(i T / n) <= x < floor((i + 1) T / n)
-  const int i0 = (int)(((first + 1) * blocks - 1) / total), i1 = (int)(((first + per) * blocks - 1) / total);
+  const int i0 = runs.of(first), i1 = runs.of(first + per - 1);
   const float* part = a.part + (size_t)g * (D + 2);
   const size_t step = (size_t)a.G * (D + 2);
   float m = -INFINITY, l = 0.f, o = 0.f;

@@ -418,7 +418,7 @@ int socket_soft_count_attend(const void* Q, const void* V, sk_dtype kv, const vo
  * given, below lens[b]; the other rows of the cache (and of the outputs) stay as
  * they are.
  * O is f32 unless said otherwise, its layout as Q's. G = Hq / Hkv <= 8 and
- * B * Hkv <= 65535 in all of them. ws must be 16-byte aligned.
+ * B * Hkv <= 65535 in all of them. ws, O and scales must be 16-byte aligned.
  */
 
 /*
