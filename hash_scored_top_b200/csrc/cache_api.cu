@@ -104,7 +104,7 @@ int rows_splits(int pairs, int R, int n) {
 // tiles to give each of their warps one.
 int stream_blocks(int pairs, int n) {
   const long long tiles = (long long)pairs * ((n + 31) / 32);
-  return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + SA_WARPS - 1) / SA_WARPS));
+  return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + 11) / 12));
 }
 
 // Workspace of the attention of R rows per pair: the larger of what its
@@ -140,11 +140,11 @@ int launch_stream(const CacheAttendParams& p, int B, float* O, bool pdl, cudaStr
   constexpr bool CAN_LIST = FMT != KV_BF16;
   if (CAN_LIST && p.mode == KEYS_LISTED) {
     SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32, CAN_LIST>>(SH::SMEM)));
-    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, CAN_LIST>, dim3(blocks), SA_THREADS, SH::SMEM, s, pdl,
+    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, CAN_LIST>, dim3(blocks), SH::THREADS, SH::SMEM, s, pdl,
                   "stream_attend_kernel", sp, B));
   } else {
     SK_TRY((allow_smem<stream_attend_kernel<D, FMT, QF32, false>>(SH::SMEM)));
-    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, false>, dim3(blocks), SA_THREADS, SH::SMEM, s, pdl,
+    SK_TRY(launch(stream_attend_kernel<D, FMT, QF32, false>, dim3(blocks), SH::THREADS, SH::SMEM, s, pdl,
                   "stream_attend_kernel", sp, B));
   }
   return launch(stream_merge_kernel<D, SH::TILE>, dim3(p.G, B * p.Hkv), 4 * D, 0, s, true, "stream_merge_kernel", sp, O, B,

@@ -9,18 +9,22 @@
 //     sequences are. A run that crosses a pair's end gives a partial
 //     (m, l, o[D]) per head for each side; stream_merge_kernel joins a pair's
 //     partials in order.
-//   * A tile (32 positions, 16 for bf16 with D = 128) is a warp's own work.
-//     Each lane copies (cp.async, 16 bytes) just the bytes of K and V that it
-//     will use itself to a slot of its own in shared memory: no barriers, no
-//     bank conflicts, and the next tile in flight costs no registers. Only the
-//     scales of a tile are shared by the lanes.
-//   * Tensor cores, m16n8k16. S[rows x keys] = Q . K^T has the heads in rows
-//     0..7 of M; rows 8..15 carry the low parts of an f32 query. S's
-//     accumulators are P's operand as they are: rows 0..7 its high parts, rows
-//     8..15 its low parts, so that one product per 8 columns of V gives both.
-//     The order of the head dimension inside S's products and of the columns
-//     of O is free, so a lane's 16 bytes of K are its operand, and its 16 bytes
-//     of four V rows are the four contraction rows of 16 (bf16: 8) columns.
+//   * A tile (32 positions, 16 for bf16 with D = 128) is a warp's own work,
+//     copied to the warp's own stages in shared memory (cp.async): no block
+//     barriers, and the next tile in flight costs no registers. Every copy
+//     instruction of a warp takes 512 bytes in a row where the rows lie so:
+//     with 64-byte pieces of eight rows to an instruction, so that each lane
+//     copied what it used, reads ended at 5.1 TB/s of 7.2. 16-byte chunks are
+//     placed so that the operands' reads do not meet in a bank.
+//   * Tensor cores, m16n8k16. S[heads x keys] = Q . K^T has the heads in rows
+//     0..7 of M; rows 8..15 carry the low parts of an f32 query. O^T[D x heads]
+//     = V^T . P^T has P on the N side, and S's accumulators are that operand as
+//     they lie: a lane's two keys of head r. The order of the head dimension
+//     inside S's products and of the columns of O is free, so a lane's 16 bytes
+//     of K are its operand, and its 16 bytes of four V rows are the four
+//     contraction rows of 16 (bf16: 8) columns. (P on the M side, its high and
+//     low parts in rows 0..7 and 8..15, takes as many products but twice the
+//     accumulators: 64 registers, which spilled.)
 //   * 8-bit codes become f16 exactly. Queries are scaled by a power of two to
 //     fill f16 (an 11-bit high part holds a bf16 value; an f32 one takes two).
 //     A key's scale multiplies its logit, a value's scale its weight; weights
@@ -34,27 +38,34 @@
 
 namespace hst {
 
-constexpr int SA_WARPS = 12;
-constexpr int SA_THREADS = 32 * SA_WARPS;
-
-// A stage of a warp's ring: HALVES x 16 positions, each of CHUNKS x 512 bytes
-// (16 per lane) and the scales of its 16 rows.
+// A stage of a warp's ring: HALVES x 16 positions, each of 16 K rows, 16 V rows
+// and their scales.
 template <int D, int FMT>
 struct StreamShape {
   static constexpr bool B16 = FMT == KV_BF16;
-  static constexpr int ROW = B16 ? 2 * D : D;             // bytes of a cache row
+  static constexpr int ROW = B16 ? 2 * D : D;             // bytes of a cache row: 64, 128 or 256
   static constexpr int KC = ROW / 64;                     // 16-byte chunks of a K row per lane (4 lanes a row)
-  static constexpr int VB = ROW / 8;                      // bytes of a V row per lane (8 lanes a row): 32, 16 or 8
-  static constexpr int VC = VB >= 16 ? 4 * (VB / 16) : 2; // chunks of the lane's four V rows
-  static constexpr int CHUNKS = 2 * KC + VC;
-  static constexpr int HALF = CHUNKS * 512 + (B16 ? 0 : 128);
+  static constexpr int VB = ROW / 8;                      // bytes of a V row per lane (8 lanes a row): 8, 16 or 32
+  static constexpr int HALF = 32 * ROW + (B16 ? 0 : 128);
   static constexpr int HALVES = HALF > 8000 ? 1 : 2;
+  static constexpr int WARPS = 12;
+  static constexpr int THREADS = 32 * WARPS;
   static constexpr int TILE = 16 * HALVES;                // positions
   static constexpr int STAGE = HALVES * HALF;
   // 12 warps x 2 stages of 8 KB, or 3 of the 4 KB of 8 bits and D = 64
   static constexpr int STAGES = STAGE > 6000 ? 2 : 3;
-  static constexpr int SMEM = SA_WARPS * STAGES * STAGE;
+  static constexpr int SMEM = WARPS * STAGES * STAGE;
   static_assert(STAGES * STAGE >= (8 * D + 16) * 4, "a warp's partial lies in its own stages");
+
+  // Place of chunk j of row n (of 16) among the K or V rows of a half. K is
+  // read chunk c (+ 4 i) of rows r: two neighbouring rows in a phase of eight
+  // lanes; V chunk r (+ 8 k) of rows 2 c: four rows, every other one.
+  __host__ __device__ static constexpr int k_place(int n, int j) {
+    return ROW == 64 ? 64 * n + 16 * j : ROW * n + 16 * (j ^ (4 * (n & 1)));
+  }
+  __host__ __device__ static constexpr int v_place(int n, int j) {
+    return ROW == 64 ? 128 * (n >> 1) + 16 * ((4 * (n & 1) + j) ^ (2 * ((n >> 1) & 3))) : ROW * n + 16 * (j ^ (n & 6));
+  }
 };
 
 struct StreamParams {
@@ -95,8 +106,14 @@ struct StreamRuns {
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (mma_bf16_16816 of attend.cuh, free to be moved)
+__device__ __forceinline__ void mma_b16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -153,10 +170,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 template <int D, int FMT, bool QF32, bool LISTED>
-__global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const StreamParams sp, int B) {
+__global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend_kernel(const StreamParams sp, int B) {
   using SH = StreamShape<D, FMT>;
   constexpr bool B16 = SH::B16;
-  constexpr int KS = D / 16, NT = D / 8;                   // steps of Q.K, column tiles of O
+  constexpr int KS = D / 16, NT = D / 16;                  // steps of Q.K, column tiles of O
+  constexpr int SA_WARPS = SH::WARPS, SA_THREADS = SH::THREADS;
   constexpr int KC = SH::KC, STAGES = SH::STAGES, HALVES = SH::HALVES, ROW = SH::ROW, TILE = SH::TILE;
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ float sm_w[SA_WARPS][8];                      // a warp's factor in the block's partial
@@ -185,9 +203,12 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
     const int te = min(per, ta + (t1 - t0));
     const int len = seq_len(a.lens, b, a.N);
     const size_t base = (size_t)pair * a.Ncap;
-    const unsigned char* Kp = reinterpret_cast<const unsigned char*>(a.K) + base * ROW + 16 * c;
-    const unsigned char* Vp = reinterpret_cast<const unsigned char*>(a.V) + base * ROW + (SH::VB >= 16 ? 16 : 8) * r;
+    const unsigned char* Kp = reinterpret_cast<const unsigned char*>(a.K) + base * ROW;
+    const unsigned char* Vp = reinterpret_cast<const unsigned char*>(a.V) + base * ROW;
     const float* Sp = a.scales + 2 * base;
+    // a copy instruction i of a warp takes bytes 512 i + 16 lane of a half's rows
+    constexpr int CP = ROW / 32;
+    const int lane_n = 16 * lane / ROW, lane_j = lane % (ROW / 16);
 
     // ---- the copies of a tile. Listed: lane i holds position i's row. Else a half's 16 positions are 16 rows from
     // `row` on, the first `cnt` of which are seen.
@@ -233,75 +254,42 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
       uint32_t bits = 0u;
 #pragma unroll
       for (int hf = 0; hf < HALVES; ++hf) {
-        const uint32_t dst = ring + (uint32_t)(stage * SH::STAGE + hf * SH::HALF) + 16u * lane;
-        const uint32_t sdst = ring + (uint32_t)(stage * SH::STAGE + hf * SH::HALF + SH::CHUNKS * 512);
+        const uint32_t dst = ring + (uint32_t)(stage * SH::STAGE + hf * SH::HALF), sdst = dst + 32u * ROW;
         if constexpr (LISTED) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int kr = __shfl_sync(FULL, nl, 16 * hf + r + 8 * n);
-            const unsigned char* src = Kp + (size_t)max(kr, 0) * ROW;
-#pragma unroll
-            for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * (n * KC + i), src + 64 * i, kr >= 0 ? 16 : 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int vr = __shfl_sync(FULL, nl, 16 * hf + 2 * c + (i & 1) + 8 * (i >> 1));
-            const unsigned char* src = Vp + (size_t)max(vr, 0) * ROW;
-            if constexpr (SH::VB == 8) {
-              async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src, vr >= 0 ? 8 : 0);
-            } else {
-#pragma unroll
-              for (int k = 0; k < SH::VB / 16; ++k)
-                async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + 128 * k, vr >= 0 ? 16 : 0);
-            }
+          for (int i = 0; i < CP; ++i) {
+            const int n = (512 * i) / ROW + lane_n;
+            const int row = __shfl_sync(FULL, nl, 16 * hf + n);
+            const size_t at = (size_t)max(row, 0) * ROW + 16 * lane_j;
+            const int on = row >= 0 ? 16 : 0;
+            async_copy16(dst + SH::k_place(n, lane_j), Kp + at, on);
+            async_copy16(dst + 16u * ROW + SH::v_place(n, lane_j), Vp + at, on);
           }
           if constexpr (!B16) {
-            const int sr = __shfl_sync(FULL, nl, 16 * hf + (lane & 15));
-            if (lane < 16) async_copy8(sdst + 8u * lane, Sp + 2 * (size_t)max(sr, 0), sr >= 0 ? 8 : 0);
+            const int row = __shfl_sync(FULL, nl, 16 * hf + (lane & 15));
+            if (lane < 16) async_copy8(sdst + 8u * lane, Sp + 2 * (size_t)max(row, 0), row >= 0 ? 8 : 0);
           }
         } else {
           const Half x = nx[hf];
           bits |= ((1u << x.cnt) - 1u) << (16 * hf);
-          const unsigned char* ks = Kp + ((size_t)x.row + r) * ROW;
-          const unsigned char* vs = Vp + ((size_t)x.row + 2 * c) * ROW;
+          const size_t at = (size_t)x.row * ROW + 16 * lane;
           if (x.cnt == 16) {                               // the common case: constant offsets
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int i = 0; i < KC; ++i) async_copy16(dst + 512u * (n * KC + i), ks + 8 * n * ROW + 64 * i);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const unsigned char* src = vs + ((i & 1) + 8 * (i >> 1)) * ROW;
-              if constexpr (SH::VB == 8) {
-                async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src);
-              } else {
-#pragma unroll
-                for (int k = 0; k < SH::VB / 16; ++k)
-                  async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + 128 * k);
-              }
+            for (int i = 0; i < CP; ++i) {
+              const int n = (512 * i) / ROW + lane_n;
+              async_copy16(dst + SH::k_place(n, lane_j), Kp + at + 512 * i);
+              async_copy16(dst + 16u * ROW + SH::v_place(n, lane_j), Vp + at + 512 * i);
             }
             if constexpr (!B16)
               if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + 2 * lane));
           } else {                                         // rows past the end are not read: zeros
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int i = 0; i < KC; ++i) {
-                const bool on = r + 8 * n < x.cnt;
-                async_copy16(dst + 512u * (n * KC + i), on ? ks + 8 * n * ROW + 64 * i : Kp, on ? 16 : 0);
-              }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = (i & 1) + 8 * (i >> 1);
-              const bool on = 2 * c + j < x.cnt;
-              const unsigned char* src = on ? vs + j * ROW : Vp;
-              if constexpr (SH::VB == 8) {
-                async_copy8(dst + 512u * (2 * KC + (i >> 1)) + 8u * (i & 1), src, on ? 8 : 0);
-              } else {
-#pragma unroll
-                for (int k = 0; k < SH::VB / 16; ++k)
-                  async_copy16(dst + 512u * (2 * KC + i * (SH::VB / 16) + k), src + (on ? 128 * k : 0), on ? 16 : 0);
-              }
+            for (int i = 0; i < CP; ++i) {
+              const int n = (512 * i) / ROW + lane_n;
+              const bool on = n < x.cnt;
+              const size_t from = on ? at + 512 * i : 0;
+              async_copy16(dst + SH::k_place(n, lane_j), Kp + from, on ? 16 : 0);
+              async_copy16(dst + 16u * ROW + SH::v_place(n, lane_j), Vp + from, on ? 16 : 0);
             }
             if constexpr (!B16)
               if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + min(2 * lane, 14)), min(max(8 * (x.cnt - 2 * lane), 0), 16));
@@ -382,9 +370,10 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
         async_commit();
       }
       async_wait<STAGES - 1>();
-      if constexpr (!B16) __syncwarp();                    // the scales were copied by other lanes
-      const uint32_t src = ring + (uint32_t)(stage * SH::STAGE) + 16u * lane;
-      const uint32_t ssrc = ring + (uint32_t)(stage * SH::STAGE + SH::CHUNKS * 512) + 16u * c;
+      __syncwarp();                                        // other lanes' copies too
+      const uint32_t src = ring + (uint32_t)(stage * SH::STAGE);
+      const uint32_t ksrc = src + SH::k_place(r, c), ssrc = src + 32u * ROW + 16u * c;
+      const uint32_t vsrc0 = src + 16u * ROW + (SH::VB == 8 ? SH::v_place(2 * c, r >> 1) + 8u * (r & 1) : SH::v_place(2 * c, r));
       stage = stage == STAGES - 1 ? 0 : stage + 1;
       const uint32_t live = seen[STAGES - 1];
 
@@ -396,12 +385,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
       for (int i2 = 0; i2 < KC; ++i2) {
 #pragma unroll
         for (int n = 0; n < 2 * HALVES; ++n) {
-          const uint4 v = lds128(src + (uint32_t)((n >> 1) * SH::HALF) + 512u * ((n & 1) * KC + i2));
+          // chunk 4 i2 + c of row r + 8 (n & 1): k_place's exclusive or reaches the 64s only
+          const uint4 v = lds128((ROW == 64 ? ksrc : (ksrc ^ (64u * (i2 & 1)))  + 128u * (i2 >> 1)) + (uint32_t)((n >> 1) * SH::HALF + 8 * ROW * (n & 1)));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if constexpr (B16) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              mma_bf16_16816(S[n], qh[2 * i2 + u][0], 0u, qh[2 * i2 + u][1], 0u, w[2 * u], w[2 * u + 1]);
+              mma_b16_16816(S[n], qh[2 * i2 + u][0], 0u, qh[2 * i2 + u][1], 0u, w[2 * u], w[2 * u + 1]);
           } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -461,12 +451,14 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
           vf = nf;
           E = e;
         }
+        // the accumulators are those of heads 2c and 2c + 1, whose factors lie in lanes 8c and 8c + 4
+        const float f0 = __shfl_sync(FULL, f, 8 * c), f1 = __shfl_sync(FULL, f, 8 * c + 4);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          acc[j][0] *= f;
-          acc[j][1] *= f;
-          acc[j][2] *= f;
-          acc[j][3] *= f;
+          acc[j][0] *= f0;
+          acc[j][1] *= f1;
+          acc[j][2] *= f0;
+          acc[j][3] *= f1;
         }
       }
       const float ms = m == -INFINITY ? 0.f : m;           // no finite logit yet: all weights are 0
@@ -481,22 +473,20 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
       // ---- O += P . V, half by half, column tile by column tile
 #pragma unroll
       for (int hf = 0; hf < HALVES; ++hf) {
-        const uint32_t vsrc = src + (uint32_t)(hf * SH::HALF) + 512u * (2 * KC);
-        uint32_t pa[4], pl[2] = {0u, 0u};                  // operand: rows 0..7 high, rows 8..15 low parts
+        const uint32_t vsrc = vsrc0 + (uint32_t)(hf * SH::HALF);      // rows 2c, 2c + 1, 2c + 8, 2c + 9 from here
+        uint32_t p0[2], p1[2], p2[2];                      // the weights' terms, two keys to a word
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float x = w[4 * hf + 2 * k], y = w[4 * hf + 2 * k + 1];
           if constexpr (B16) {
-            const uint32_t hi = pack_bf16x2(x, y);
-            const float x1 = x - bf16lo_to_f32(hi), y1 = y - bf16hi_to_f32(hi);
-            const uint32_t mid = pack_bf16x2(x1, y1);
-            pa[2 * k] = hi;
-            pa[2 * k + 1] = mid;
-            pl[k] = pack_bf16x2(x1 - bf16lo_to_f32(mid), y1 - bf16hi_to_f32(mid));
+            p0[k] = pack_bf16x2(x, y);
+            const float x1 = x - bf16lo_to_f32(p0[k]), y1 = y - bf16hi_to_f32(p0[k]);
+            p1[k] = pack_bf16x2(x1, y1);
+            p2[k] = pack_bf16x2(x1 - bf16lo_to_f32(p1[k]), y1 - bf16hi_to_f32(p1[k]));
           } else {
-            pa[2 * k] = pack_f16x2(x, y);
-            const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&pa[2 * k]));
-            pa[2 * k + 1] = pack_f16x2(x - hi.x, y - hi.y);
+            p0[k] = pack_f16x2(x, y);
+            const float2 hi = __half22float2(*reinterpret_cast<__half2*>(&p0[k]));
+            p1[k] = pack_f16x2(x - hi.x, y - hi.y);
           }
         }
         if constexpr (B16) {
@@ -505,18 +495,19 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
             uint32_t v[4][4];
 #pragma unroll
             for (int i2 = 0; i2 < 4; ++i2) {
-              const uint4 x = lds128(vsrc + 512u * (i2 * (SH::VB / 16) + k));
+              const uint4 x = lds128(vsrc + (uint32_t)(ROW * ((i2 & 1) + 8 * (i2 >> 1)) + 128 * k));
               v[i2][0] = x.x;
               v[i2][1] = x.y;
               v[i2][2] = x.z;
               v[i2][3] = x.w;
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int sel = j & 1 ? 0x7632 : 0x5410;
-              const uint32_t b0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], sel), b1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], sel);
-              mma_bf16_16816(acc[8 * k + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
-              mma_bf16_16816(acc[8 * k + j], pl[0], 0u, pl[1], 0u, b0, b1);
+            for (int j = 0; j < 4; ++j) {                  // columns 2 j, 2 j + 1 of the lane's eight
+              const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
+              mma_b16_16816(acc[4 * k + j], a0, a1, a2, a3, p0[0], p0[1]);
+              mma_b16_16816(acc[4 * k + j], a0, a1, a2, a3, p1[0], p1[1]);
+              mma_b16_16816(acc[4 * k + j], a0, a1, a2, a3, p2[0], p2[1]);
             }
           }
         } else {
@@ -524,7 +515,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
           if constexpr (SH::VB == 16) {
 #pragma unroll
             for (int i2 = 0; i2 < 4; ++i2) {
-              const uint4 x = lds128(vsrc + 512u * i2);
+              const uint4 x = lds128(vsrc + (uint32_t)(ROW * ((i2 & 1) + 8 * (i2 >> 1))));
               v[i2][0] = x.x;
               v[i2][1] = x.y;
               v[i2][2] = x.z;
@@ -532,29 +523,27 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
             }
           } else {
 #pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2) {
-              const uint4 x = lds128(vsrc + 512u * i2);
-              v[2 * i2][0] = x.x;
-              v[2 * i2][1] = x.y;
-              v[2 * i2 + 1][0] = x.z;
-              v[2 * i2 + 1][1] = x.w;
+            for (int i2 = 0; i2 < 4; ++i2) {               // the odd rows of a pair lie 64 bytes off, by exclusive or
+              const uint2 x = lds64((i2 & 1 ? vsrc ^ 64u : vsrc) + 512u * (i2 >> 1));
+              v[i2][0] = x.x;
+              v[i2][1] = x.y;
             }
           }
 #pragma unroll
           for (int q = 0; q < SH::VB / 4; ++q) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {                  // columns 4 q + 2 u, 4 q + 2 u + 1
+            for (int u = 0; u < 2; ++u) {                  // columns 4 q + 2 u, 4 q + 2 u + 1 of the lane's
               const int sel = u ? 0x7362 : 0x5140;
               const uint32_t x = __byte_perm(v[0][q], v[1][q], sel), y = __byte_perm(v[2][q], v[3][q], sel);
-              mma_f16_16816(acc[4 * q + 2 * u], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, false>(x),
-                            codes_to_f16x2<FMT, false>(y));
-              mma_f16_16816(acc[4 * q + 2 * u + 1], pa[0], pa[1], pa[2], pa[3], codes_to_f16x2<FMT, true>(x),
-                            codes_to_f16x2<FMT, true>(y));
+              const uint32_t a0 = codes_to_f16x2<FMT, false>(x), a1 = codes_to_f16x2<FMT, true>(x);
+              const uint32_t a2 = codes_to_f16x2<FMT, false>(y), a3 = codes_to_f16x2<FMT, true>(y);
+              mma_f16_16816(acc[2 * q + u], a0, a1, a2, a3, p0[0], p0[1]);
+              mma_f16_16816(acc[2 * q + u], a0, a1, a2, a3, p1[0], p1[1]);
             }
           }
         }
       }
-      if constexpr (!B16) __syncwarp();                    // every lane has read the scales: they may be overwritten
+      __syncwarp();                                        // every lane has read the stage: it may be overwritten
     }
     async_wait<0>();
 
@@ -563,19 +552,18 @@ __global__ void __launch_bounds__(SA_THREADS, 1) stream_attend_kernel(const Stre
     l += __shfl_xor_sync(FULL, l, 2);
     float* mine_s = reinterpret_cast<float*>(dyn + (size_t)warp * STAGES * SH::STAGE);
     __syncwarp();                                          // other lanes' slots of the ring are done with
-    if (r < G) {
-      if (c == 0) {
-        mine_s[r] = m;
-        mine_s[8 + r] = l;
-      }
+    if (r < G && c == 0) {
+      mine_s[r] = m;
+      mine_s[8 + r] = l;
+    }
+    {
       const float of = B16 ? 1.f : 1.f / vf;               // a power of two
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int n = 2 * c + k;                         // the lane row whose column this is
-          const int col = B16 ? 64 * (j >> 3) + 8 * n + (j & 7) : SH::VB * n + j;
-          mine_s[16 + r * D + col] = (acc[j][k] + acc[j][2 + k]) * of;
+        for (int k = 0; k < 4; ++k) {                      // head 2c + (k & 1), second column of the two for k >= 2
+          const int col = (B16 ? 64 * (j >> 2) + 8 * r + 2 * (j & 3) : SH::VB * r + 2 * j) + (k >> 1);
+          if (2 * c + (k & 1) < G) mine_s[16 + (2 * c + (k & 1)) * D + col] = acc[j][k] * of;
         }
       }
     }
