@@ -682,11 +682,13 @@ size_t select_ws_bytes(const FusedPlan& fp, int pairs, int Ncap, int L) {
   return align256(table_image_bytes(pairs, L)) + align256((size_t)pairs * Ncap * 4);
 }
 
+}  // namespace
+
 // 2-D tensor map of a [rows][d] bf16 matrix for TMA tiles of 64 columns x
 // box_rows rows with the 128-byte swizzle (the layout the tcgen05 hash
 // kernel's operands use). The driver's encoder is looked up once through the
 // runtime.
-int encode_rows_map(CUtensorMap* map, const void* base, long rows, int d, int box_rows) {
+int hst::encode_rows_map(CUtensorMap* map, const void* base, long rows, int d, int box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -707,6 +709,8 @@ int encode_rows_map(CUtensorMap* map, const void* base, long rows, int d, int bo
   if (r != CUDA_SUCCESS) return fail(SK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return SK_OK;
 }
+
+namespace {
 
 constexpr int kAppendMaxKeys = 16;
 

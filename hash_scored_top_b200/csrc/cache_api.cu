@@ -11,6 +11,7 @@
 #include "cache_attend.cuh"
 #include "quant.cuh"
 #include "stream_attend.cuh"
+#include "tree_attend.cuh"
 
 using namespace hst;
 
@@ -107,6 +108,14 @@ int stream_blocks(int pairs, int n) {
   return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + 11) / 12));
 }
 
+// Groups of query rows that the tree kernel takes at once: 128, or with more
+// rows 256 (two tiles that share each K and V tile).
+int tree_groups(int R) { return R <= 128 ? 1 : (R + 255) / 256; }
+
+size_t tree_bytes(int pairs, int R, int d) {
+  return align256((size_t)(kNumSMs + (size_t)pairs * tree_groups(R)) * 2 * std::min(R, 128) * (d + 2) * sizeof(float));
+}
+
 // Workspace of the attention of R rows per pair: the larger of what its
 // kernels need (the query does not know the cache's format).
 size_t attend_bytes(int pairs, int R, int n, int d) {
@@ -159,6 +168,39 @@ int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, fl
                          : (f ? launch_stream<D, KV_E4M3, true>(p, B, O, pdl, s) : launch_stream<D, KV_E4M3, false>(p, B, O, pdl, s));
 }
 
+// Drafted tokens over a bf16 cache, on tcgen05. f32 outputs take three terms of
+// the weights and, for the tensor memory that they need, tiles of 64 keys.
+template <int D, int KT, int NT, bool WIDE, typename OT>
+int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
+  using SH = TreeShape<D, KT, WIDE>;
+  TreeParams p;
+  p.a = a;
+  p.groups = tree_groups(a.T * a.G);
+  p.rows = std::min(a.T * a.G, 128);
+  const int pairs = B * a.Hkv;
+  const long long tiles = (long long)pairs * p.groups * ((a.n + KT - 1) / KT);
+  const int blocks = (int)std::min((long long)kNumSMs, tiles);
+  CUtensorMap mk, mv;
+  SK_TRY(encode_rows_map(&mk, a.K, (long)pairs * a.Ncap, D, KT));
+  SK_TRY(encode_rows_map(&mv, a.V, (long)pairs * a.Ncap, D, KT));
+  SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE>>(SH::SMEM)));
+  SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE>, dim3(blocks), TR_THREADS, SH::SMEM, s, false, "tree_attend_kernel", p, B,
+                mk, mv));
+  return launch(tree_merge_kernel<D, KT, WIDE, OT>, dim3(a.T * a.G, pairs), 4 * D, 0, s, true, "tree_merge_kernel", p, O, B,
+                blocks);
+}
+
+template <int D>
+int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStream_t s) {
+  const bool wide = a.T * a.G > 128;
+  if (o == SK_BF16) {
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
+    return wide ? launch_tree<D, 128, 1, true>(a, B, out, s) : launch_tree<D, 128, 1, false>(a, B, out, s);
+  }
+  float* out = reinterpret_cast<float*>(O);
+  return wide ? launch_tree<D, 64, 3, true>(a, B, out, s) : launch_tree<D, 64, 3, false>(a, B, out, s);
+}
+
 template <int D>
 int launch_rows(const CacheAttendParams& p, sk_dtype kv, int pairs, bool pdl, cudaStream_t s) {
   const dim3 grid(p.splits, p.T * p.G, pairs);
@@ -182,6 +224,8 @@ int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float sca
   if (kv != SK_F32 && p.mode != KEYS_TREE)
     return d == 128 ? stream_attend<128>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s)
                     : stream_attend<64>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s);
+  if (kv == SK_BF16 && p.mode == KEYS_TREE)
+    return d == 128 ? tree_attend<128>(p, B, O, o, s) : tree_attend<64>(p, B, O, o, s);
   p.splits = rows_splits(pairs, R, p.n);
   SK_TRY(d == 128 ? launch_rows<128>(p, kv, pairs, pdl, s) : launch_rows<64>(p, kv, pairs, pdl, s));
   CacheMergeParams m;
@@ -314,7 +358,7 @@ size_t hst::cache_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int 
     }
     case SK_OP_TREE_DECODE:
       if (k < 1 || k > kMaxDrafts || N < 0 || N > INT_MAX - k) return bad;
-      return attend_bytes(pairs, k * G, N + k, d);
+      return std::max(attend_bytes(pairs, k * G, N + k, d), tree_bytes(pairs, k * G, d));
     default:
       return bad;
   }
@@ -538,6 +582,8 @@ int tree_decode(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtyp
   if (T < 1 || T > kMaxDrafts) return fail(SK_ERR_UNSUPPORTED, "T=%d: 1 <= T <= %d drafted tokens", T, kMaxDrafts);
   if (N < 0 || (long long)N + T > Ncap)
     return fail(SK_ERR_INVALID_ARG, "N=%d cached and T=%d drafted keys do not fit Ncap=%d", N, T, Ncap);
+  if ((long long)B * Hkv * Ncap > INT_MAX - 128)
+    return fail(SK_ERR_UNSUPPORTED, "a cache of more than 2^31 - 129 rows (B * Hkv * Ncap)");
   SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_TREE_DECODE, B, Hq, Hkv, Ncap, N, d, 0, T)));
   CacheAttendParams p = cache_params(Q, K, V, scales, lens, Hq, Hkv, Ncap, N);
   p.mode = KEYS_TREE;

@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/hash_scored_top.h"
@@ -72,6 +73,10 @@ inline int check_dtype(sk_dtype t) {
     if (reinterpret_cast<uintptr_t>(ptr) % (bytes))                                              \
       return fail(SK_ERR_INVALID_ARG, "%s must be %d-byte aligned", #ptr, (int)(bytes));         \
   } while (0)
+
+// 2-D tensor map of a [rows][d] bf16 matrix: TMA tiles of 64 columns x box_rows
+// rows with the 128-byte swizzle. (api.cu)
+HST_HIDDEN int encode_rows_map(CUtensorMap* map, const void* base, long rows, int d, int box_rows);
 
 // ---- cache_api.cu, for api.cu
 // Workspace of the operators over quantised, block-selected and drafted caches.

@@ -1,0 +1,562 @@
+// Attention of T drafted tokens over a bf16 cache on tcgen05 (tree_decode; see
+// cache_attend.cuh for what a token sees).
+//
+// A KV head's R = T * G query rows are the M side of two products per tile of
+// KT keys: S[128 x KT] = Q . K^T and O[128 x D] += P . V. A cache byte is used by
+// all rows at once, so up to about a hundred rows the cache's bytes bound the
+// kernel (4 D per key and pair), beyond that the two products (4 D R flops).
+//
+// Roles of a block (one per SM, 320 threads):
+//   warp 8    copies K and V tiles by TMA (128-byte swizzle) into a ring of
+//             slots, K and V alternating;
+//   warp 9    issues the MMAs: S of a job into tensor memory, and, when its
+//             weights are there, O += P . V with P as the tensor-memory operand
+//             and V as it lies (N-major);
+//   warps 0-3 and 4-7 are two groups of 128 softmax threads, a thread per row
+//             and lane of tensor memory. They take turns, so that one's softmax
+//             runs beside the other's MMAs. With R <= 128 they share the rows
+//             and take every other tile, each with an O of its own; with more
+//             rows (WIDE) each has 128 rows of its own and takes every tile.
+// S is read from tensor memory twice (the maximum, then the weights), which keeps
+// the weights of a chunk in registers, not a row's. They are written over the chunk of
+// S that they came from. O is rescaled only when a row's maximum has grown by
+// more than 2^8 since the last time: weights up to 2^8 lose nothing.
+// The weights enter the second product as NT bf16 terms: one for bf16 outputs
+// (each is off by at most 2^-8, as the output's own rounding is), three (24
+// bits) for f32.
+//
+// The list of all (pair, group of rows, tile) is cut into one even run per
+// block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
+// each side, which tree_merge_kernel joins in order.
+//
+// Drafted keys lie behind the cached ones, in the last tiles. Their S is masked
+// per row. A V row that is not finite must reach only the rows that see it,
+// which a product cannot do (0 * NaN): such rows (and the rows behind the
+// sequence) are cleared in shared memory, and what a drafted one gives to the
+// rows that see it is added at the end, in plain arithmetic.
+#pragma once
+
+#include "cache_attend.cuh"
+#include "stream_attend.cuh"
+#include "tcgen05.cuh"
+
+namespace hst {
+
+constexpr int TR_THREADS = 320;
+constexpr int TR_MAX_SLOTS = 12;
+constexpr uint32_t TR_SMEM_MAX = 231424;     // dynamic; 1 KB of static shared memory besides
+constexpr int TR_MAX_DRAFT_WORDS = 8;
+
+template <int D, int KT, bool WIDE>
+struct TreeShape {
+  static constexpr int QBYTES = 128 * D * 2;               // one Q tile
+  static constexpr int SLOT = KT * D * 2;                  // one K or V tile
+  static constexpr int QTILES = WIDE ? 2 : 1;
+  static constexpr int FIT = ((int)TR_SMEM_MAX - QTILES * QBYTES) / SLOT;
+  static constexpr int SLOTS = FIT < TR_MAX_SLOTS ? FIT : TR_MAX_SLOTS;
+  static constexpr int SMEM = QTILES * QBYTES + SLOTS * SLOT;
+  static_assert(SLOTS >= 4, "two tiles in flight");
+};
+
+struct TreeParams {
+  CacheAttendParams a;
+  int groups;                // groups of 128 (WIDE: 256) rows of a pair
+  int rows;                  // rows of a partial: min(R, 128)
+};
+
+// Tiles of a sequence's units: its cached and its drafted keys.
+template <int KT>
+__device__ __forceinline__ int tree_tiles(const CacheAttendParams& a, int b) {
+  return (seq_len(a.lens, b, a.N) + a.T + KT - 1) / KT;
+}
+
+template <int KT>
+__device__ __forceinline__ StreamRuns tree_runs(const TreeParams& p, int B, int blocks) {
+  StreamRuns s;
+  s.total = 0;
+  for (int b = 0; b < B; ++b) s.total += p.a.Hkv * p.groups * tree_tiles<KT>(p.a, b);
+  s.q = (int)((uint32_t)s.total / (uint32_t)blocks);
+  s.rem = s.total - s.q * blocks;
+  return s;
+}
+
+// Bits of the positions j0 .. j0 + 31 that the token sees.
+struct TreeRow {
+  const uint32_t* mask;      // the token's words, or null: a chain
+  int t, len, T;
+  __device__ __forceinline__ uint32_t drafts(int w) const {      // drafted keys 32 w ..
+    const int left = T - 32 * w;
+    if (left <= 0 || w < 0) return 0u;
+    const uint32_t in = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+    if (mask) return __ldg(mask + w) & in;
+    const int n = t + 1 - 32 * w;
+    return n >= 32 ? in : n <= 0 ? 0u : ((1u << n) - 1u) & in;
+  }
+  __device__ __forceinline__ uint32_t sees(int j0) const {
+    const int a = len - j0;                                      // cached positions from here
+    if (a >= 32) return 0xffffffffu;
+    if (a > 0) return ((1u << a) - 1u) | (drafts(0) << a);
+    const int w = (-a) >> 5, s = (-a) & 31;
+    return s == 0 ? drafts(w) : (drafts(w) >> s) | (drafts(w + 1) << (32 - s));
+  }
+};
+
+// D[tmem] (+)= A[tmem] . B[smem], bf16: A is M x 16, two values to a column; B N-major.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Operand descriptor of an N-major tile with the 128-byte swizzle: atoms of 64
+// columns x 8 rows (rows 128 bytes apart), `lbo` bytes between atoms along the
+// columns and `sbo` along the rows.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// f32 accumulators, bf16 operands, M = 128; B is N-major if b_mn.
+__device__ __forceinline__ constexpr uint32_t tree_idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+template <int D, int KT, int NT, bool WIDE>
+__global__ void __launch_bounds__(TR_THREADS, 1)
+    tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
+  using SH = TreeShape<D, KT, WIDE>;
+  constexpr int NS = SH::SLOTS, ATOMS = D / 64;
+  // tensor memory: S (and P over it) of group w at w * SCOLS, its O at 256 + w * D. Chunk q of 32 keys holds S at
+  // 32 q, then the first two terms of P at 32 q and 32 q + 16, the third at KT + 16 q.
+  constexpr uint32_t SCOLS = NT == 3 ? KT + KT / 2 : KT, OCOL = 256;
+  static_assert(2 * SCOLS <= OCOL && OCOL + 2 * D <= 512, "tensor memory");
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 8];
+  // drafted keys whose V a group cleared, by the parity of the segment: a thread clears its words for a segment while
+  // others may still read the last one's
+  __shared__ uint32_t bad_s[2][2][TR_MAX_DRAFT_WORDS];
+  __shared__ uint32_t tbase_s;
+  const CacheAttendParams& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t s0 = smem_u32(dyn), q0 = s0, slots = s0 + SH::QTILES * SH::QBYTES;
+  const uint32_t b0 = smem_u32(bars), full = b0, empty = b0 + 8 * TR_MAX_SLOTS, sfull = b0 + 16 * TR_MAX_SLOTS;
+  const uint32_t pready = sfull + 16, qready = sfull + 32, odone = sfull + 40, drain = sfull + 48;
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tbase_s), 512u);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, WIDE ? 2 : 1);              // one commit per job of the tile
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(sfull + 8 * w, 1);
+      mbar_init(pready + 8 * w, 128);
+    }
+    mbar_init(qready, 256);
+    mbar_init(odone, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tb = tbase_s;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // the block's run, walked by every role on its own
+  const StreamRuns runs = tree_runs<KT>(p, B, gridDim.x);
+  const int t1 = runs.begin(blockIdx.x + 1);
+  struct Segment {
+    int t0, b, first;                                      // walking state
+    int unit, pair, grp, len, ta, te;
+  };
+  auto next_segment = [&](Segment& s) -> bool {
+    if (s.t0 >= t1) return false;
+    int per;
+    for (;; ++s.b) {
+      per = tree_tiles<KT>(a, s.b);
+      const int all = a.Hkv * p.groups * per;
+      if (s.t0 - s.first < all) break;
+      s.first += all;
+    }
+    const int u = (s.t0 - s.first) / per;
+    s.unit = s.b * a.Hkv * p.groups + u;
+    s.pair = s.unit / p.groups;
+    s.grp = s.unit % p.groups;
+    s.len = seq_len(a.lens, s.b, a.N);
+    s.ta = s.t0 - s.first - u * per;
+    s.te = min(per, s.ta + (t1 - s.t0));
+    s.t0 += s.te - s.ta;
+    return true;
+  };
+  Segment seg = {};
+  seg.t0 = runs.begin(blockIdx.x);
+  const int R = a.T * a.G;
+  // slot and phase of the n-th K or V tile of the block
+  auto slot_of = [&](int n) { return slots + (uint32_t)(n % NS) * (uint32_t)SH::SLOT; };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- copies
+    int n = 0;
+    if (lane == 0) {
+      bool ok = true;
+      while (ok && next_segment(seg)) {
+        for (int i = seg.ta; i < seg.te && ok; ++i) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int s = n % NS;
+            if (n >= NS && !mbar_wait_bounded(empty + 8 * s, (uint32_t)((n / NS - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)SH::SLOT);
+#pragma unroll
+            for (int at = 0; at < ATOMS; ++at)
+              tma_load_2d(slot_of(n) + (uint32_t)(at * KT * 128), kv ? &mapV : &mapK, 64 * at, seg.pair * a.Ncap + i * KT,
+                          full + 8 * s);
+          }
+        }
+      }
+      // nothing stays in flight, whatever the others did
+      for (int j = max(0, n - NS); j < n; ++j) mbar_wait_bounded(full + 8 * (j % NS), (uint32_t)((j / NS) & 1));
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      bool ok = true;
+      int tile0 = 0, seg_n = 0, jobs_of[2] = {0, 0};
+      constexpr uint32_t idS = tree_idesc(KT, false), idO = tree_idesc(D, true);
+      auto waits = [&](uint32_t bar, int n) {
+        ok = ok && mbar_wait_bounded(bar, (uint32_t)(n & 1));
+        return ok;
+      };
+      while (ok && next_segment(seg)) {
+        const int nt = seg.te - seg.ta, njobs = WIDE ? 2 * nt : nt;
+        if (!waits(qready, seg_n)) break;
+        auto issue_s = [&](int j) {
+          const int w = j & 1, n = 2 * (tile0 + (WIDE ? j >> 1 : j));
+          if (!waits(full + 8 * (n % NS), n / NS)) return;
+          tc_fence_after_sync();
+          const uint32_t ks = slot_of(n), qs = q0 + (WIDE ? (uint32_t)(w * SH::QBYTES) : 0u);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            tc_mma_bf16(tb + w * SCOLS, umma_desc_sw128(qs + (uint32_t)((s >> 2) * 128 * 128 + (s & 3) * 32), 1024u),
+                        umma_desc_sw128(ks + (uint32_t)((s >> 2) * KT * 128 + (s & 3) * 32), 1024u), idS, s > 0 ? 1u : 0u);
+          tc_commit(sfull + 8 * w);
+          tc_commit(empty + 8 * (n % NS));
+        };
+        issue_s(0);
+        if (njobs > 1) issue_s(1);
+        for (int j = 0; j < njobs && ok; ++j) {
+          const int w = j & 1, tile = WIDE ? j >> 1 : j, n = 2 * (tile0 + tile) + 1;
+          if (!waits(full + 8 * (n % NS), n / NS)) break;
+          if (!waits(pready + 8 * w, jobs_of[w])) break;
+          ++jobs_of[w];
+          tc_fence_after_sync();
+          const uint32_t vs = slot_of(n);
+          const bool first = j < 2;                        // each group's first job
+#pragma unroll
+          for (int s = 0; s < KT / 16; ++s) {
+            const uint64_t bd = umma_desc_sw128_mn(vs + (uint32_t)(s * 2048), KT * 128u, 1024u);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+              const uint32_t at = k < 2 ? 32u * (s >> 1) + 16u * k + 8u * (s & 1) : KT + 8u * s;
+              tc_mma_ts(tb + OCOL + w * D, tb + w * SCOLS + at, bd, idO, first && s == 0 && k == 0 ? 0u : 1u);
+            }
+          }
+          tc_commit(empty + 8 * (n % NS));
+          if (j + 2 < njobs) issue_s(j + 2);
+        }
+        if (!ok) break;
+        tc_commit(odone);
+        tile0 += nt;
+        ++seg_n;
+      }
+      tc_commit(drain);                                    // every MMA issued is done before tensor memory is freed
+      mbar_wait_bounded(drain, 0u);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int w = warp >> 2, row = tid & 127;              // group, and row of its tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tb + lanes + w * SCOLS, to = tb + lanes + OCOL + w * D;
+    bool ok = true;
+    int tile0 = 0, seg_n = 0, jobs = 0;
+    while (ok && next_segment(seg)) {
+      const int nt = seg.te - seg.ta;
+      const int h = seg.pair % a.Hkv;
+      const int my_row = (WIDE ? 256 * seg.grp + 128 * w : 128 * seg.grp) + row;      // of the pair's R
+      const bool live = my_row < R;
+      const int t = live ? my_row / a.G : 0, g = live ? my_row % a.G : 0;
+      uint32_t(*bad)[TR_MAX_DRAFT_WORDS] = bad_s[seg_n & 1];
+      const TreeRow vis = {a.mask ? a.mask + ((size_t)seg.b * a.T + t) * a.mask_words : nullptr, t, seg.len, a.T};
+      const size_t qrow = ((size_t)seg.b * a.T + t) * a.Hq + h * a.G + g;
+      // ---- Q: WIDE each group its own tile, else the two groups half of the columns each
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D);
+        const uint32_t dst = q0 + (WIDE ? (uint32_t)(w * SH::QBYTES) : 0u) + (uint32_t)row * 128u;
+        constexpr int C = D / 8;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (!WIDE && (c & 1) != w) continue;
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ row) & 7) * 16)),
+                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        }
+        if (row < TR_MAX_DRAFT_WORDS) bad[w][row] = 0u;
+        fence_proxy_async_shared();
+        mbar_arrive(qready);
+      }
+      float m = -INFINITY, l = 0.f;
+      int done = 0;                                        // this group's jobs of the segment
+      for (int i = WIDE ? 0 : w; i < nt; i += WIDE ? 1 : 2) {
+        const int j0 = (seg.ta + i) * KT;
+        const bool tail = j0 + KT > seg.len;
+        if (!mbar_wait_bounded(sfull + 8 * w, (uint32_t)(jobs & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        // ---- the row's maximum
+        float mt = -INFINITY;
+#pragma unroll 2
+        for (int q = 0; q < KT / 32; ++q) {
+          uint32_t v[32];
+          tmem_ld32(ts + 32u * q, v);
+          const uint32_t see = tail ? vis.sees(j0 + 32 * q) : 0xffffffffu;
+          if (!tail) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, __uint_as_float(v[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) : -INFINITY);
+          }
+        }
+        // a negative scale turns the order round: take the smallest product instead
+        if (a.scale_log2 < 0.f) {
+          mt = INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < KT / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(ts + 32u * q, v);
+            const uint32_t see = vis.sees(j0 + 32 * q);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mt = fminf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) : INFINITY);
+          }
+          if (mt == INFINITY) mt = -INFINITY / a.scale_log2;      // nothing seen
+        }
+        mt *= a.scale_log2;
+        if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m))) {
+          const float mn = fmaxf(m, mt);
+          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (done > 0) {                                  // S is done, so is the product before it: O is at rest
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t v[32];
+              tmem_ld32(to + 32u * q, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+              uint32_t x[16], y[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                x[k] = v[k];
+                y[k] = v[16 + k];
+              }
+              tmem_st16(to + 32u * q, x);
+              tmem_st16(to + 32u * q + 16u, y);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        // ---- weights, chunk by chunk over the S that they come from
+#pragma unroll 1
+        for (int q = 0; q < KT / 32; ++q) {
+          uint32_t v[32], t0[16], t1v[16], t2[16];
+          tmem_ld32(ts + 32u * q, v);
+          const uint32_t see = tail ? vis.sees(j0 + 32 * q) : 0xffffffffu;
+          float ls = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float x = ex2(fmaf(__uint_as_float(v[k]), a.scale_log2, -ms)), y = ex2(fmaf(__uint_as_float(v[k + 1]), a.scale_log2, -ms));
+            if (tail) {
+              if (!((see >> k) & 1u)) x = 0.f;
+              if (!((see >> (k + 1)) & 1u)) y = 0.f;
+            }
+            ls += x + y;
+            t0[k / 2] = pack_bf16x2(x, y);
+            if constexpr (NT == 3) {
+              const float x1 = x - bf16lo_to_f32(t0[k / 2]), y1 = y - bf16hi_to_f32(t0[k / 2]);
+              t1v[k / 2] = pack_bf16x2(x1, y1);
+              t2[k / 2] = pack_bf16x2(x1 - bf16lo_to_f32(t1v[k / 2]), y1 - bf16hi_to_f32(t1v[k / 2]));
+            }
+          }
+          l += ls;
+          tmem_st16(ts + 32u * q, t0);
+          if constexpr (NT == 3) {
+            tmem_st16(ts + 32u * q + 16u, t1v);
+            tmem_st16(ts + KT + 16u * q, t2);
+          }
+        }
+        // ---- the rows of V that a product must not meet (WIDE: the first group, whose product with a tile comes first)
+        if (tail && (!WIDE || w == 0)) {
+          const int n = 2 * (tile0 + i) + 1;
+          if (!mbar_wait_bounded(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) {
+            ok = false;
+            break;
+          }
+          const int pos = j0 + row;
+          if (row < KT && pos >= seg.len) {
+            const uint32_t vr = slot_of(n) + (uint32_t)row * 128u;
+            bool clear = pos >= seg.len + a.T;
+            if (!clear) {
+              bool odd = false;
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 x = lds128(vr + (uint32_t)((c >> 3) * KT * 128 + ((c ^ row) & 7) * 16));
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  odd |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
+              }
+              if (odd) {
+                atomicOr(&bad[w][(pos - seg.len) >> 5], 1u << ((pos - seg.len) & 31));
+                clear = true;
+              }
+            }
+            if (clear) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (uint32_t)((c >> 3) * KT * 128 + c % 8 * 16)), "r"(0u)
+                             : "memory");
+            }
+          }
+          fence_proxy_async_shared();
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(pready + 8 * w);
+        ++jobs;
+        ++done;
+      }
+      if (!ok) break;
+      if (!mbar_wait_bounded(odone, (uint32_t)(seg_n & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      // ---- this group's partial of the row
+      float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * 2 + w) * p.rows + row) * (D + 2);
+      const bool any_bad = [&] {
+        uint32_t x = 0u;
+#pragma unroll
+        for (int k = 0; k < TR_MAX_DRAFT_WORDS; ++k) x |= bad[WIDE ? 0 : w][k];
+        return x != 0u;
+      }();
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        if (done > 0) {
+          tmem_ld32(to + 32u * q, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0u;
+        }
+        if (any_bad && live) {                             // rare: drafted keys left out of the products
+          for (int i = 0; i < a.T; ++i) {
+            if (!((bad[WIDE ? 0 : w][i >> 5] >> (i & 31)) & 1u) || !((vis.drafts(i >> 5) >> (i & 31)) & 1u)) continue;
+            const size_t kr = ((size_t)seg.pair * a.Ncap + seg.len + i) * D;
+            const __nv_bfloat16 *qp = reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D,
+                                *kp = reinterpret_cast<const __nv_bfloat16*>(a.K) + kr,
+                                *vp = reinterpret_cast<const __nv_bfloat16*>(a.V) + kr + 32 * q;
+            float s = 0.f;
+            for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(qp[c]), __bfloat162float(kp[c]), s);
+            const float x = ex2(s * a.scale_log2 - (m == -INFINITY ? 0.f : m));
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(x, __bfloat162float(vp[k]), __uint_as_float(v[k])));
+          }
+        }
+        if (row < p.rows) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) *reinterpret_cast<uint2*>(out + 2 + 32 * q + k) = make_uint2(v[k], v[k + 1]);
+        }
+      }
+      if (row < p.rows) *reinterpret_cast<float2*>(out) = make_float2(m, l);
+      tc_fence_before_sync();                              // O has been read before the next segment's products
+      tile0 += nt;
+      ++seg_n;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc(tb, 512u);
+  }
+}
+
+// Joins a row's partials in order. grid = (R, pairs); four groups of D threads take a quarter of the partials each.
+template <int D, int KT, bool WIDE, typename OT>
+__global__ void __launch_bounds__(4 * D) tree_merge_kernel(const TreeParams p, OT* O, int B, int blocks) {
+  __shared__ float sm[4], sl[4], so[4][D];
+  const CacheAttendParams& a = p.a;
+  const int my_row = blockIdx.x, pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
+  const int col = threadIdx.x % D, part4 = threadIdx.x / D;
+  const int per = tree_tiles<KT>(a, b);
+  const StreamRuns runs = tree_runs<KT>(p, B, blocks);
+  const int grp = my_row / (WIDE ? 256 : 128), row = my_row % 128, w = WIDE ? (my_row >> 7) & 1 : 0;
+  const int unit = pair * p.groups + grp;
+  int first = (h * p.groups + grp) * per;                  // the unit's first tile
+  for (int i = 0; i < b; ++i) first += a.Hkv * p.groups * tree_tiles<KT>(a, i);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i0 = runs.of(first), i1 = runs.of(first + per - 1);
+  // WIDE: a partial of each block; else one of each group of each block
+  const int n = (i1 - i0 + 1) * (WIDE ? 1 : 2);
+  float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int k = part4; k < n; k += 4) {
+    const int i = i0 + (WIDE ? k : k >> 1), x = WIDE ? w : k & 1;
+    const float* q = a.part + (((size_t)(i + unit) * 2 + x) * p.rows + row) * (D + 2);
+    const float pm = __ldcg(q), pl = __ldcg(q + 1), po = __ldcg(q + 2 + col);
+    const float mn = fmaxf(m, pm);
+    const float f0 = mn == -INFINITY ? 1.f : ex2(m - mn), f1 = mn == -INFINITY ? 1.f : ex2(pm - mn);
+    m = mn;
+    l = fmaf(f1, pl, l * f0);
+    o = fmaf(f1, po, o * f0);
+  }
+  if (col == 0) {
+    sm[part4] = m;
+    sl[part4] = l;
+  }
+  so[part4][col] = o;
+  __syncthreads();
+  if (part4 > 0) return;
+  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  l = o = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = mm == -INFINITY ? 1.f : ex2(sm[k] - mm);
+    l = fmaf(f, sl[k], l);
+    o = fmaf(f, so[k][col], o);
+  }
+  const size_t at = (((size_t)b * a.T + my_row / a.G) * a.Hq + h * a.G + my_row % a.G) * D + col;
+  O[at] = (OT)(l == 0.f ? 0.f : o / l);
+}
+
+}  // namespace hst
