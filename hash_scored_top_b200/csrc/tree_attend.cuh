@@ -36,6 +36,8 @@
 // rows that see it is added at the end, in plain arithmetic.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_attend.cuh"
 #include "stream_attend.cuh"
 #include "tcgen05.cuh"
@@ -131,6 +133,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Pairs of f32 in one register pair, and the three-way maximum.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float v;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
 }
 
 template <int D, int KT, int NT, bool WIDE>
@@ -334,33 +359,30 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         tc_fence_after_sync();
         // ---- the row's maximum
         float mt = -INFINITY;
+        if (!tail && a.scale_log2 >= 0.f) {
 #pragma unroll 2
-        for (int q = 0; q < KT / 32; ++q) {
-          uint32_t v[32];
-          tmem_ld32(ts + 32u * q, v);
-          const uint32_t see = tail ? vis.sees(j0 + 32 * q) : 0xffffffffu;
-          if (!tail) {
+          for (int q = 0; q < KT / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(ts + 32u * q, v);
+            float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);      // two chains
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, __uint_as_float(v[k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) : -INFINITY);
+            for (int k = 2; k < 32; k += 4) {
+              x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              if (k + 2 < 32) y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
+            mt = max3(mt, x, y);
           }
-        }
-        // a negative scale turns the order round: take the smallest product instead
-        if (a.scale_log2 < 0.f) {
-          mt = INFINITY;
+          mt *= a.scale_log2;
+        } else {                                           // masked, or an order that the scale turns round
 #pragma unroll 1
           for (int q = 0; q < KT / 32; ++q) {
             uint32_t v[32];
             tmem_ld32(ts + 32u * q, v);
             const uint32_t see = vis.sees(j0 + 32 * q);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fminf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) : INFINITY);
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) * a.scale_log2 : -INFINITY);
           }
-          if (mt == INFINITY) mt = -INFINITY / a.scale_log2;      // nothing seen
         }
-        mt *= a.scale_log2;
         if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m))) {
           const float mn = fmaxf(m, mt);
           const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -386,34 +408,46 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         }
         const float ms = m == -INFINITY ? 0.f : m;
         // ---- weights, chunk by chunk over the S that they come from
+        auto weights = [&](auto mask_tag) {
+          constexpr bool masked = decltype(mask_tag)::value;
+          const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ms2 = pack_f32x2(-ms, -ms);
+          uint64_t sum = 0ull;                             // (0, 0)
 #pragma unroll 1
-        for (int q = 0; q < KT / 32; ++q) {
-          uint32_t v[32], t0[16], t1v[16], t2[16];
-          tmem_ld32(ts + 32u * q, v);
-          const uint32_t see = tail ? vis.sees(j0 + 32 * q) : 0xffffffffu;
-          float ls = 0.f;
+          for (int q = 0; q < KT / 32; ++q) {
+            uint32_t v[32], t0[16];
+            [[maybe_unused]] uint32_t t1v[16], t2[16];
+            tmem_ld32(ts + 32u * q, v);
+            [[maybe_unused]] const uint32_t see = masked ? vis.sees(j0 + 32 * q) : 0u;
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float x = ex2(fmaf(__uint_as_float(v[k]), a.scale_log2, -ms)), y = ex2(fmaf(__uint_as_float(v[k + 1]), a.scale_log2, -ms));
-            if (tail) {
-              if (!((see >> k) & 1u)) x = 0.f;
-              if (!((see >> (k + 1)) & 1u)) y = 0.f;
+            for (int k = 0; k < 32; k += 2) {
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sc2, ms2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              if constexpr (masked) {
+                if (!((see >> k) & 1u)) x = 0.f;
+                if (!((see >> (k + 1)) & 1u)) y = 0.f;
+              }
+              sum = add_f32x2(sum, pack_f32x2(x, y));
+              t0[k / 2] = pack_bf16x2(x, y);
+              if constexpr (NT == 3) {
+                const float x1 = x - bf16lo_to_f32(t0[k / 2]), y1 = y - bf16hi_to_f32(t0[k / 2]);
+                t1v[k / 2] = pack_bf16x2(x1, y1);
+                t2[k / 2] = pack_bf16x2(x1 - bf16lo_to_f32(t1v[k / 2]), y1 - bf16hi_to_f32(t1v[k / 2]));
+              }
             }
-            ls += x + y;
-            t0[k / 2] = pack_bf16x2(x, y);
+            tmem_st16(ts + 32u * q, t0);
             if constexpr (NT == 3) {
-              const float x1 = x - bf16lo_to_f32(t0[k / 2]), y1 = y - bf16hi_to_f32(t0[k / 2]);
-              t1v[k / 2] = pack_bf16x2(x1, y1);
-              t2[k / 2] = pack_bf16x2(x1 - bf16lo_to_f32(t1v[k / 2]), y1 - bf16hi_to_f32(t1v[k / 2]));
+              tmem_st16(ts + 32u * q + 16u, t1v);
+              tmem_st16(ts + KT + 16u * q, t2);
             }
           }
-          l += ls;
-          tmem_st16(ts + 32u * q, t0);
-          if constexpr (NT == 3) {
-            tmem_st16(ts + 32u * q + 16u, t1v);
-            tmem_st16(ts + KT + 16u * q, t2);
-          }
-        }
+          float x, y;
+          unpack_f32x2(sum, x, y);
+          l += x + y;
+        };
+        if (tail) weights(std::true_type{});
+        else weights(std::false_type{});
         // ---- the rows of V that a product must not meet (WIDE: the first group, whose product with a tile comes first)
         if (tail && (!WIDE || w == 0)) {
           const int n = 2 * (tile0 + i) + 1;
