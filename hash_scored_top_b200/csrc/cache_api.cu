@@ -108,12 +108,17 @@ int stream_blocks(int pairs, int n) {
   return (int)std::max(1LL, std::min((long long)kNumSMs, (tiles + 11) / 12));
 }
 
-// Groups of query rows that the tree kernel takes at once: 128, or with more
-// rows 256 (two tiles that share each K and V tile).
-int tree_groups(int R) { return R <= 128 ? 1 : (R + 255) / 256; }
+// Query rows that a block of the tree kernel takes at once: 128, or, for more
+// rows and bf16 outputs, 256 (two teams that share each K and V tile).
+bool tree_wide(int R, sk_dtype o) { return R > 128 && o == SK_BF16; }
+int tree_groups(int R, bool wide) { return wide ? (R + 255) / 256 : (R + 127) / 128; }
 
+// Partials: (blocks + units) runs, each of one or two teams' rows.
 size_t tree_bytes(int pairs, int R, int d) {
-  return align256((size_t)(kNumSMs + (size_t)pairs * tree_groups(R)) * 2 * std::min(R, 128) * (d + 2) * sizeof(float));
+  size_t most = 0;
+  for (int wide = 0; wide < (R > 128 ? 2 : 1); ++wide)
+    most = std::max(most, (kNumSMs + (size_t)pairs * tree_groups(R, wide)) * (wide ? 2 : 1));
+  return align256(most * std::min(R, 128) * (d + 2) * sizeof(float));
 }
 
 // Workspace of the attention of R rows per pair: the larger of what its
@@ -168,14 +173,13 @@ int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, fl
                          : (f ? launch_stream<D, KV_E4M3, true>(p, B, O, pdl, s) : launch_stream<D, KV_E4M3, false>(p, B, O, pdl, s));
 }
 
-// Drafted tokens over a bf16 cache, on tcgen05. f32 outputs take three terms of
-// the weights and, for the tensor memory that they need, tiles of 64 keys.
+// Drafted tokens over a bf16 cache, on tcgen05.
 template <int D, int KT, int NT, bool WIDE, typename OT>
 int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
   using SH = TreeShape<D, KT, WIDE>;
   TreeParams p;
   p.a = a;
-  p.groups = tree_groups(a.T * a.G);
+  p.groups = tree_groups(a.T * a.G, WIDE);
   p.rows = std::min(a.T * a.G, 128);
   const int pairs = B * a.Hkv;
   const long long tiles = (long long)pairs * p.groups * ((a.n + KT - 1) / KT);
@@ -186,19 +190,16 @@ int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
   SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE>>(SH::SMEM)));
   SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE>, dim3(blocks), TR_THREADS, SH::SMEM, s, false, "tree_attend_kernel", p, B,
                 mk, mv));
-  return launch(tree_merge_kernel<D, KT, WIDE, OT>, dim3(a.T * a.G, pairs), 4 * D, 0, s, true, "tree_merge_kernel", p, O, B,
+  return launch(tree_merge_kernel<D, KT, WIDE, OT>, dim3((a.T * a.G + TREE_MERGE_ROWS - 1) / TREE_MERGE_ROWS, pairs),
+                32 * TREE_MERGE_ROWS, 0, s, true, "tree_merge_kernel", p, O, B,
                 blocks);
 }
 
 template <int D>
 int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStream_t s) {
-  const bool wide = a.T * a.G > 128;
-  if (o == SK_BF16) {
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
-    return wide ? launch_tree<D, 128, 1, true>(a, B, out, s) : launch_tree<D, 128, 1, false>(a, B, out, s);
-  }
-  float* out = reinterpret_cast<float*>(O);
-  return wide ? launch_tree<D, 64, 3, true>(a, B, out, s) : launch_tree<D, 64, 3, false>(a, B, out, s);
+  if (o == SK_F32) return launch_tree<D, 128, 3, false>(a, B, reinterpret_cast<float*>(O), s);
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
+  return tree_wide(a.T * a.G, o) ? launch_tree<D, 64, 1, true>(a, B, out, s) : launch_tree<D, 128, 1, false>(a, B, out, s);
 }
 
 template <int D>

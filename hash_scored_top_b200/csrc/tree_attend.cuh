@@ -12,18 +12,21 @@
 //   warp 9    issues the MMAs: S of a job into tensor memory, and, when its
 //             weights are there, O += P . V with P as the tensor-memory operand
 //             and V as it lies (N-major);
-//   warps 0-3 and 4-7 are two groups of 128 softmax threads, a thread per row
-//             and lane of tensor memory. They take turns, so that one's softmax
-//             runs beside the other's MMAs. With R <= 128 they share the rows
-//             and take every other tile, each with an O of its own; with more
-//             rows (WIDE) each has 128 rows of its own and takes every tile.
-// S is read from tensor memory twice (the maximum, then the weights), which keeps
-// the weights of a chunk in registers, not a row's. They are written over the chunk of
-// S that they came from. O is rescaled only when a row's maximum has grown by
-// more than 2^8 since the last time: weights up to 2^8 lose nothing.
+//   warps 0-7 are softmax threads, one row (lane of tensor memory) each. Up to
+//             128 rows are one team of 256: two threads share a row, half of a
+//             tile's columns each, and exchange the half maxima. More rows (WIDE)
+//             are two teams of 128 threads and rows, which share the tiles.
+// S has two buffers per team: the product of the next tile runs while the
+// weights of this one are taken (with one buffer a tile took S, softmax and P . V
+// one after the other: 5100 clocks per 128 keys where the cache's bytes take
+// 2500). The weights are written over the S that they come from. O is rescaled
+// only when a row's maximum has grown by more than 2^8 since the last time: weights
+// up to 2^8 lose nothing.
 // The weights enter the second product as NT bf16 terms: one for bf16 outputs
 // (each is off by at most 2^-8, as the output's own rounding is), three (24
-// bits) for f32.
+// bits) for f32. Tensor memory holds O and two buffers of S and the third term:
+// 128 + 2 * 192 columns for a team of 128 rows and D = 128; two teams fit with tiles of
+// 64 keys and one term, so f32 outputs of more than 128 rows are taken 128 at a time.
 //
 // The list of all (pair, group of rows, tile) is cut into one even run per
 // block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
@@ -57,7 +60,7 @@ struct TreeShape {
   static constexpr int FIT = ((int)TR_SMEM_MAX - QTILES * QBYTES) / SLOT;
   static constexpr int SLOTS = FIT < TR_MAX_SLOTS ? FIT : TR_MAX_SLOTS;
   static constexpr int SMEM = QTILES * QBYTES + SLOTS * SLOT;
-  static_assert(SLOTS >= 4, "two tiles in flight");
+  static_assert(SLOTS >= 6, "the tiles of both buffers and one in flight");
 };
 
 struct TreeParams {
@@ -103,20 +106,30 @@ struct TreeRow {
   }
 };
 
-// D[tmem] (+)= A[tmem] . B[smem], bf16: A is M x 16, two values to a column; B N-major.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The operand descriptors of this kernel are those of umma_desc_sw128 (K-major)
+// and, for V as it lies, N-major with the 128-byte swizzle: atoms of 64 columns
+// x 8 rows (rows 128 bytes apart), `lbo` bytes between atoms along the columns
+// and 1024 along the rows. Their upper words are the same for all tiles; an MMA
+// then costs its thread one addition per operand. (Building the descriptors for
+// every MMA took the issuing thread 105 clocks each, which bound the kernel.)
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);         // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+
+// D[tmem] (+)= A[smem] . B[smem]^T, bf16, both K-major.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHi)
       : "memory");
 }
-// Operand descriptor of an N-major tile with the 128-byte swizzle: atoms of 64
-// columns x 8 rows (rows 128 bytes apart), `lbo` bytes between atoms along the
-// columns and `sbo` along the rows.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) |
-         (1ull << 46) | (2ull << 61);
+// D[tmem] (+)= A[tmem] . B[smem], bf16: A is M x 16, two values to a column; B N-major.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHi)
+      : "memory");
 }
 // f32 accumulators, bf16 operands, M = 128; B is N-major if b_mn.
 __device__ __forceinline__ constexpr uint32_t tree_idesc(int n, bool b_mn) {
@@ -133,6 +146,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
 }
 
 // Pairs of f32 in one register pair, and the three-way maximum.
@@ -162,22 +181,24 @@ template <int D, int KT, int NT, bool WIDE>
 __global__ void __launch_bounds__(TR_THREADS, 1)
     tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
   using SH = TreeShape<D, KT, WIDE>;
-  constexpr int NS = SH::SLOTS, ATOMS = D / 64;
-  // tensor memory: S (and P over it) of group w at w * SCOLS, its O at 256 + w * D. Chunk q of 32 keys holds S at
+  constexpr int NS = SH::SLOTS, ATOMS = D / 64, TEAMS = WIDE ? 2 : 1, TEAM = WIDE ? 128 : 256;
+  // tensor memory: O of team w at w * D; buffer sb of its S (and P over it) behind them. Chunk q of 32 keys holds S at
   // 32 q, then the first two terms of P at 32 q and 32 q + 16, the third at KT + 16 q.
-  constexpr uint32_t SCOLS = NT == 3 ? KT + KT / 2 : KT, OCOL = 256;
-  static_assert(2 * SCOLS <= OCOL && OCOL + 2 * D <= 512, "tensor memory");
+  constexpr uint32_t SCOLS = NT == 3 ? KT + KT / 2 : KT;
+  static_assert(TEAMS * (D + 2 * SCOLS) <= 512, "tensor memory");
+  auto s_col = [](int w, int sb) { return (uint32_t)(TEAMS * D) + (uint32_t)(2 * w + sb) * SCOLS; };
   extern __shared__ __align__(1024) unsigned char dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 8];
-  // drafted keys whose V a group cleared, by the parity of the segment: a thread clears its words for a segment while
-  // others may still read the last one's
-  __shared__ uint32_t bad_s[2][2][TR_MAX_DRAFT_WORDS];
+  __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 16];
+  // drafted keys whose V was cleared, by the parity of the segment: they are cleared for a segment while others may
+  // still read the last one's
+  __shared__ uint32_t bad_s[2][TR_MAX_DRAFT_WORDS];
+  __shared__ float half_s[2][2][128];                      // maxima (at the end sums) of half a row, by the parity of the tile
   __shared__ uint32_t tbase_s;
   const CacheAttendParams& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
   const uint32_t s0 = smem_u32(dyn), q0 = s0, slots = s0 + SH::QTILES * SH::QBYTES;
   const uint32_t b0 = smem_u32(bars), full = b0, empty = b0 + 8 * TR_MAX_SLOTS, sfull = b0 + 16 * TR_MAX_SLOTS;
-  const uint32_t pready = sfull + 16, qready = sfull + 32, odone = sfull + 40, drain = sfull + 48;
+  const uint32_t pready = sfull + 32, pvdone = sfull + 64, qready = sfull + 96, halves = sfull + 104, drain = sfull + 112;
   if (warp == 0) {
     tmem_alloc(smem_u32(&tbase_s), 512u);
     tmem_relinquish();
@@ -185,14 +206,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, WIDE ? 2 : 1);              // one commit per job of the tile
+      mbar_init(empty + 8 * i, TEAMS);                     // one commit per team
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(sfull + 8 * w, 1);
-      mbar_init(pready + 8 * w, 128);
+    for (int i = 0; i < 4; ++i) {                          // team w, buffer sb: 2 w + sb
+      mbar_init(sfull + 8 * i, 1);
+      mbar_init(pready + 8 * i, TEAM);
+      mbar_init(pvdone + 8 * i, 1);
     }
     mbar_init(qready, 256);
-    mbar_init(odone, 1);
+    mbar_init(halves, 256);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -232,13 +254,15 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   Segment seg = {};
   seg.t0 = runs.begin(blockIdx.x);
   const int R = a.T * a.G;
-  // slot and phase of the n-th K or V tile of the block
+  // J counts the block's tiles: their K and V lie in slots 2 J and 2 J + 1 (modulo the ring), their S in buffer J & 1
   auto slot_of = [&](int n) { return slots + (uint32_t)(n % NS) * (uint32_t)SH::SLOT; };
+  auto bar_of = [](uint32_t bars4, int w, int J) { return bars4 + 8u * (uint32_t)(2 * w + (J & 1)); };
+  auto par_of = [](int J) { return (uint32_t)((J >> 1) & 1); };
 
   if (warp == 8) {
     // ---------------------------------------------------------------- copies
-    int n = 0;
     if (lane == 0) {
+      int n = 0;
       bool ok = true;
       while (ok && next_segment(seg)) {
         for (int i = seg.ta; i < seg.te && ok; ++i) {
@@ -262,54 +286,56 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
+    // elect.sync, not a lane's number: the compiler then knows that one thread is left and keeps the operands in
+    // uniform registers (an MMA costs its thread 85 clocks instead of 125, with nothing else between them)
+    if (elect_one()) {
       bool ok = true;
-      int tile0 = 0, seg_n = 0, jobs_of[2] = {0, 0};
+      int J0 = 0, seg_n = 0;
       constexpr uint32_t idS = tree_idesc(KT, false), idO = tree_idesc(D, true);
-      auto waits = [&](uint32_t bar, int n) {
-        ok = ok && mbar_wait_bounded(bar, (uint32_t)(n & 1));
+      auto waits = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(bar, parity);
         return ok;
       };
+      auto issue_s = [&](int w, int J) {
+        const int n = 2 * J;
+        if (!waits(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) return;
+        tc_fence_after_sync();
+        const uint32_t ks = desc_lo(slot_of(n), 16u), qs = desc_lo(q0 + (uint32_t)(w * SH::QBYTES), 16u), sd = tb + s_col(w, J & 1);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          tc_mma_ss(sd, qs + (uint32_t)(((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
+                    ks + (uint32_t)(((s >> 2) * KT * 128 + (s & 3) * 32) >> 4), idS, s > 0);
+        tc_commit(bar_of(sfull, w, J));
+        tc_commit(empty + 8 * (n % NS));
+      };
       while (ok && next_segment(seg)) {
-        const int nt = seg.te - seg.ta, njobs = WIDE ? 2 * nt : nt;
-        if (!waits(qready, seg_n)) break;
-        auto issue_s = [&](int j) {
-          const int w = j & 1, n = 2 * (tile0 + (WIDE ? j >> 1 : j));
-          if (!waits(full + 8 * (n % NS), n / NS)) return;
-          tc_fence_after_sync();
-          const uint32_t ks = slot_of(n), qs = q0 + (WIDE ? (uint32_t)(w * SH::QBYTES) : 0u);
+        const int nt = seg.te - seg.ta;
+        if (!waits(qready, (uint32_t)(seg_n & 1))) break;
+        for (int i = 0; i < 2 && i < nt; ++i)
+          for (int w = 0; w < TEAMS && ok; ++w) issue_s(w, J0 + i);
+        for (int i = 0; i < nt && ok; ++i) {
+          const int J = J0 + i, n = 2 * J + 1;
+          if (!waits(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) break;
+          const uint32_t vs = desc_lo(slot_of(n), KT * 128u);
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            tc_mma_bf16(tb + w * SCOLS, umma_desc_sw128(qs + (uint32_t)((s >> 2) * 128 * 128 + (s & 3) * 32), 1024u),
-                        umma_desc_sw128(ks + (uint32_t)((s >> 2) * KT * 128 + (s & 3) * 32), 1024u), idS, s > 0 ? 1u : 0u);
-          tc_commit(sfull + 8 * w);
-          tc_commit(empty + 8 * (n % NS));
-        };
-        issue_s(0);
-        if (njobs > 1) issue_s(1);
-        for (int j = 0; j < njobs && ok; ++j) {
-          const int w = j & 1, tile = WIDE ? j >> 1 : j, n = 2 * (tile0 + tile) + 1;
-          if (!waits(full + 8 * (n % NS), n / NS)) break;
-          if (!waits(pready + 8 * w, jobs_of[w])) break;
-          ++jobs_of[w];
-          tc_fence_after_sync();
-          const uint32_t vs = slot_of(n);
-          const bool first = j < 2;                        // each group's first job
+          for (int w = 0; w < TEAMS; ++w) {
+            if (!waits(bar_of(pready, w, J), par_of(J))) break;
+            tc_fence_after_sync();
+            const uint32_t ps = tb + s_col(w, J & 1);
 #pragma unroll
-          for (int s = 0; s < KT / 16; ++s) {
-            const uint64_t bd = umma_desc_sw128_mn(vs + (uint32_t)(s * 2048), KT * 128u, 1024u);
+            for (int s = 0; s < KT / 16; ++s) {
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-              const uint32_t at = k < 2 ? 32u * (s >> 1) + 16u * k + 8u * (s & 1) : KT + 8u * s;
-              tc_mma_ts(tb + OCOL + w * D, tb + w * SCOLS + at, bd, idO, first && s == 0 && k == 0 ? 0u : 1u);
+              for (int k = 0; k < NT; ++k) {
+                const uint32_t at = k < 2 ? 32u * (s >> 1) + 16u * k + 8u * (s & 1) : KT + 8u * s;
+                tc_mma_ts(tb + w * D, ps + at, vs + (uint32_t)(s * 2048 >> 4), idO, s > 0 || k > 0 || i > 0);
+              }
             }
+            tc_commit(bar_of(pvdone, w, J));
+            tc_commit(empty + 8 * (n % NS));
+            if (i + 2 < nt) issue_s(w, J + 2);             // over the P that the product before it reads
           }
-          tc_commit(empty + 8 * (n % NS));
-          if (j + 2 < njobs) issue_s(j + 2);
         }
-        if (!ok) break;
-        tc_commit(odone);
-        tile0 += nt;
+        J0 += nt;
         ++seg_n;
       }
       tc_commit(drain);                                    // every MMA issued is done before tensor memory is freed
@@ -317,89 +343,110 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const int w = warp >> 2, row = tid & 127;              // group, and row of its tile
+    constexpr int COLS = 64;                               // columns of a tile per thread
+    static_assert(WIDE ? KT == COLS : KT == 2 * COLS, "a thread's columns");
+    constexpr int OC = WIDE ? D : D / 2;                   // columns of O that it looks after
+    const int hw = warp >> 2, row = tid & 127;             // WIDE: team, else half of the columns; row of its tile
+    const int w = WIDE ? hw : 0, chunk0 = WIDE ? 0 : 2 * hw;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tb + lanes + w * SCOLS, to = tb + lanes + OCOL + w * D;
+    const uint32_t to = tb + lanes + w * D + (WIDE ? 0u : (uint32_t)(hw * OC));
     bool ok = true;
-    int tile0 = 0, seg_n = 0, jobs = 0;
+    int J0 = 0, seg_n = 0, exchanges = 0;
+    // the other half's value of this row (WIDE: none)
+    auto exchange = [&](float x, float& other) -> bool {
+      half_s[exchanges & 1][hw][row] = x;
+      mbar_arrive(halves);
+      if (!mbar_wait_bounded(halves, (uint32_t)(exchanges & 1))) return false;
+      other = half_s[exchanges & 1][hw ^ 1][row];
+      ++exchanges;
+      return true;
+    };
     while (ok && next_segment(seg)) {
       const int nt = seg.te - seg.ta;
       const int h = seg.pair % a.Hkv;
       const int my_row = (WIDE ? 256 * seg.grp + 128 * w : 128 * seg.grp) + row;      // of the pair's R
       const bool live = my_row < R;
       const int t = live ? my_row / a.G : 0, g = live ? my_row % a.G : 0;
-      uint32_t(*bad)[TR_MAX_DRAFT_WORDS] = bad_s[seg_n & 1];
+      uint32_t* bad = bad_s[seg_n & 1];
       const TreeRow vis = {a.mask ? a.mask + ((size_t)seg.b * a.T + t) * a.mask_words : nullptr, t, seg.len, a.T};
       const size_t qrow = ((size_t)seg.b * a.T + t) * a.Hq + h * a.G + g;
-      // ---- Q: WIDE each group its own tile, else the two groups half of the columns each
+      // ---- Q: WIDE each team its own tile, else the two halves every other chunk
       {
         const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D);
-        const uint32_t dst = q0 + (WIDE ? (uint32_t)(w * SH::QBYTES) : 0u) + (uint32_t)row * 128u;
-        constexpr int C = D / 8;
+        const uint32_t dst = q0 + (uint32_t)(w * SH::QBYTES) + (uint32_t)row * 128u;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (!WIDE && (c & 1) != w) continue;
+        for (int c = 0; c < D / 8; ++c) {
+          if (!WIDE && (c & 1) != hw) continue;
           const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ row) & 7) * 16)),
                        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
         }
-        if (row < TR_MAX_DRAFT_WORDS) bad[w][row] = 0u;
+        if (tid < TR_MAX_DRAFT_WORDS) bad[tid] = 0u;
         fence_proxy_async_shared();
         mbar_arrive(qready);
       }
       float m = -INFINITY, l = 0.f;
-      int done = 0;                                        // this group's jobs of the segment
-      for (int i = WIDE ? 0 : w; i < nt; i += WIDE ? 1 : 2) {
-        const int j0 = (seg.ta + i) * KT;
+      for (int i = 0; i < nt; ++i) {
+        const int J = J0 + i, j0 = (seg.ta + i) * KT, jc = j0 + 32 * chunk0;
         const bool tail = j0 + KT > seg.len;
-        if (!mbar_wait_bounded(sfull + 8 * w, (uint32_t)(jobs & 1))) {
+        if (!mbar_wait_bounded(bar_of(sfull, w, J), par_of(J))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
+        const uint32_t ts = tb + lanes + s_col(w, J & 1);
+        uint32_t v[2][32];
+        tmem_ld64(ts + 32u * chunk0, v[0], v[1]);
         // ---- the row's maximum
         float mt = -INFINITY;
         if (!tail && a.scale_log2 >= 0.f) {
-#pragma unroll 2
-          for (int q = 0; q < KT / 32; ++q) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32u * q, v);
-            float x = __uint_as_float(v[0]), y = __uint_as_float(v[1]);      // two chains
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float x = __uint_as_float(v[q][0]), y = __uint_as_float(v[q][1]);      // two chains
 #pragma unroll
             for (int k = 2; k < 32; k += 4) {
-              x = max3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-              if (k + 2 < 32) y = max3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+              x = max3(x, __uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1]));
+              if (k + 2 < 32) y = max3(y, __uint_as_float(v[q][k + 2]), __uint_as_float(v[q][k + 3]));
             }
             mt = max3(mt, x, y);
           }
           mt *= a.scale_log2;
         } else {                                           // masked, or an order that the scale turns round
-#pragma unroll 1
-          for (int q = 0; q < KT / 32; ++q) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32u * q, v);
-            const uint32_t see = vis.sees(j0 + 32 * q);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[k]) * a.scale_log2 : -INFINITY);
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t see = vis.sees(jc + 32 * q);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * a.scale_log2 : -INFINITY);
           }
         }
+        if constexpr (!WIDE) {
+          float other;
+          if (!exchange(mt, other)) {
+            ok = false;
+            break;
+          }
+          mt = fmaxf(mt, other);
+        }
+        // (both halves of a row come to the same answer: they have the same m and mt)
         if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m))) {
           const float mn = fmaxf(m, mt);
           const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
           m = mn;
           l *= f;
-          if (done > 0) {                                  // S is done, so is the product before it: O is at rest
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t v[32];
-              tmem_ld32(to + 32u * q, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-              uint32_t x[16], y[16];
+          if (i > 0) {                                     // once the product before has left O at rest
+            if (!mbar_wait_bounded(bar_of(pvdone, w, J - 1), par_of(J - 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < OC / 32; ++q) {
+              uint32_t o[32], x[16], y[16];
+              tmem_ld32(to + 32u * q, o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
-                x[k] = v[k];
-                y[k] = v[16 + k];
+                x[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                y[k] = __float_as_uint(__uint_as_float(o[16 + k]) * f);
               }
               tmem_st16(to + 32u * q, x);
               tmem_st16(to + 32u * q + 16u, y);
@@ -407,21 +454,20 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           }
         }
         const float ms = m == -INFINITY ? 0.f : m;
-        // ---- weights, chunk by chunk over the S that they come from
+        // ---- weights, over the S that they come from
         auto weights = [&](auto mask_tag) {
           constexpr bool masked = decltype(mask_tag)::value;
           const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ms2 = pack_f32x2(-ms, -ms);
           uint64_t sum = 0ull;                             // (0, 0)
-#pragma unroll 1
-          for (int q = 0; q < KT / 32; ++q) {
-            uint32_t v[32], t0[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t t0[16];
             [[maybe_unused]] uint32_t t1v[16], t2[16];
-            tmem_ld32(ts + 32u * q, v);
-            [[maybe_unused]] const uint32_t see = masked ? vis.sees(j0 + 32 * q) : 0u;
+            [[maybe_unused]] const uint32_t see = masked ? vis.sees(jc + 32 * q) : 0u;
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float x, y;
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sc2, ms2), x, y);
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])), sc2, ms2), x, y);
               x = ex2(x);
               y = ex2(y);
               if constexpr (masked) {
@@ -436,10 +482,11 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 t2[k / 2] = pack_bf16x2(x1 - bf16lo_to_f32(t1v[k / 2]), y1 - bf16hi_to_f32(t1v[k / 2]));
               }
             }
-            tmem_st16(ts + 32u * q, t0);
+            const uint32_t at = ts + 32u * (chunk0 + q);
+            tmem_st16(at, t0);
             if constexpr (NT == 3) {
-              tmem_st16(ts + 32u * q + 16u, t1v);
-              tmem_st16(ts + KT + 16u * q, t2);
+              tmem_st16(at + 16u, t1v);
+              tmem_st16(ts + KT + 16u * (chunk0 + q), t2);
             }
           }
           float x, y;
@@ -448,9 +495,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         };
         if (tail) weights(std::true_type{});
         else weights(std::false_type{});
-        // ---- the rows of V that a product must not meet (WIDE: the first group, whose product with a tile comes first)
-        if (tail && (!WIDE || w == 0)) {
-          const int n = 2 * (tile0 + i) + 1;
+        // ---- the rows of V that a product must not meet (the first team, whose product with a tile comes first)
+        if (tail && hw == 0) {
+          const int n = 2 * J + 1;
           if (!mbar_wait_bounded(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) {
             ok = false;
             break;
@@ -470,7 +517,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                   odd |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
               }
               if (odd) {
-                atomicOr(&bad[w][(pos - seg.len) >> 5], 1u << ((pos - seg.len) & 31));
+                atomicOr(&bad[(pos - seg.len) >> 5], 1u << ((pos - seg.len) & 31));
                 clear = true;
               }
             }
@@ -485,55 +532,54 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         }
         tmem_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(pready + 8 * w);
-        ++jobs;
-        ++done;
+        mbar_arrive(bar_of(pready, w, J));
       }
       if (!ok) break;
-      if (!mbar_wait_bounded(odone, (uint32_t)(seg_n & 1))) {
+      if constexpr (!WIDE) {
+        float other;
+        if (!exchange(l, other)) {
+          ok = false;
+          break;
+        }
+        l = hw == 0 ? l + other : other + l;
+      }
+      J0 += nt;
+      if (!mbar_wait_bounded(bar_of(pvdone, w, J0 - 1), par_of(J0 - 1))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      // ---- this group's partial of the row
-      float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * 2 + w) * p.rows + row) * (D + 2);
-      const bool any_bad = [&] {
-        uint32_t x = 0u;
+      // ---- the team's partial of the row
+      float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * TEAMS + w) * p.rows + row) * (D + 2);
+      uint32_t any_bad = 0u;
 #pragma unroll
-        for (int k = 0; k < TR_MAX_DRAFT_WORDS; ++k) x |= bad[WIDE ? 0 : w][k];
-        return x != 0u;
-      }();
+      for (int k = 0; k < TR_MAX_DRAFT_WORDS; ++k) any_bad |= bad[k];
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t v[32];
-        if (done > 0) {
-          tmem_ld32(to + 32u * q, v);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0u;
-        }
-        if (any_bad && live) {                             // rare: drafted keys left out of the products
+      for (int q = 0; q < OC / 32; ++q) {
+        const int col = (WIDE ? 0 : hw * OC) + 32 * q;
+        uint32_t o[32];
+        tmem_ld32(to + 32u * q, o);
+        if (any_bad != 0u && live) {                       // rare: drafted keys left out of the products
           for (int i = 0; i < a.T; ++i) {
-            if (!((bad[WIDE ? 0 : w][i >> 5] >> (i & 31)) & 1u) || !((vis.drafts(i >> 5) >> (i & 31)) & 1u)) continue;
+            if (!((bad[i >> 5] >> (i & 31)) & 1u) || !((vis.drafts(i >> 5) >> (i & 31)) & 1u)) continue;
             const size_t kr = ((size_t)seg.pair * a.Ncap + seg.len + i) * D;
             const __nv_bfloat16 *qp = reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D,
                                 *kp = reinterpret_cast<const __nv_bfloat16*>(a.K) + kr,
-                                *vp = reinterpret_cast<const __nv_bfloat16*>(a.V) + kr + 32 * q;
+                                *vp = reinterpret_cast<const __nv_bfloat16*>(a.V) + kr + col;
             float s = 0.f;
             for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(qp[c]), __bfloat162float(kp[c]), s);
             const float x = ex2(s * a.scale_log2 - (m == -INFINITY ? 0.f : m));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(fmaf(x, __bfloat162float(vp[k]), __uint_as_float(v[k])));
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(x, __bfloat162float(vp[k]), __uint_as_float(o[k])));
           }
         }
         if (row < p.rows) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) *reinterpret_cast<uint2*>(out + 2 + 32 * q + k) = make_uint2(v[k], v[k + 1]);
+          for (int k = 0; k < 32; k += 2) *reinterpret_cast<uint2*>(out + 2 + col + k) = make_uint2(o[k], o[k + 1]);
         }
       }
-      if (row < p.rows) *reinterpret_cast<float2*>(out) = make_float2(m, l);
+      if (row < p.rows && (WIDE || hw == 0)) *reinterpret_cast<float2*>(out) = make_float2(m, l);
       tc_fence_before_sync();                              // O has been read before the next segment's products
-      tile0 += nt;
       ++seg_n;
     }
   }
@@ -545,52 +591,50 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   }
 }
 
-// Joins a row's partials in order. grid = (R, pairs); four groups of D threads take a quarter of the partials each.
+// Joins the rows' partials in order. A warp per row, grid = (ceil(R / 8), pairs).
+constexpr int TREE_MERGE_ROWS = 8;
+
 template <int D, int KT, bool WIDE, typename OT>
-__global__ void __launch_bounds__(4 * D) tree_merge_kernel(const TreeParams p, OT* O, int B, int blocks) {
-  __shared__ float sm[4], sl[4], so[4][D];
+__global__ void __launch_bounds__(32 * TREE_MERGE_ROWS) tree_merge_kernel(const TreeParams p, OT* O, int B, int blocks) {
   const CacheAttendParams& a = p.a;
-  const int my_row = blockIdx.x, pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
-  const int col = threadIdx.x % D, part4 = threadIdx.x / D;
+  const int my_row = blockIdx.x * TREE_MERGE_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
   const int per = tree_tiles<KT>(a, b);
   const StreamRuns runs = tree_runs<KT>(p, B, blocks);
   const int grp = my_row / (WIDE ? 256 : 128), row = my_row % 128, w = WIDE ? (my_row >> 7) & 1 : 0;
   const int unit = pair * p.groups + grp;
   int first = (h * p.groups + grp) * per;                  // the unit's first tile
   for (int i = 0; i < b; ++i) first += a.Hkv * p.groups * tree_tiles<KT>(a, i);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int i0 = runs.of(first), i1 = runs.of(first + per - 1);
-  // WIDE: a partial of each block; else one of each group of each block
-  const int n = (i1 - i0 + 1) * (WIDE ? 1 : 2);
-  float m = -INFINITY, l = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int k = part4; k < n; k += 4) {
-    const int i = i0 + (WIDE ? k : k >> 1), x = WIDE ? w : k & 1;
-    const float* q = a.part + (((size_t)(i + unit) * 2 + x) * p.rows + row) * (D + 2);
-    const float pm = __ldcg(q), pl = __ldcg(q + 1), po = __ldcg(q + 2 + col);
-    const float mn = fmaxf(m, pm);
-    const float f0 = mn == -INFINITY ? 1.f : ex2(m - mn), f1 = mn == -INFINITY ? 1.f : ex2(pm - mn);
-    m = mn;
-    l = fmaf(f1, pl, l * f0);
-    o = fmaf(f1, po, o * f0);
-  }
-  if (col == 0) {
-    sm[part4] = m;
-    sl[part4] = l;
-  }
-  so[part4][col] = o;
-  __syncthreads();
-  if (part4 > 0) return;
-  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  l = o = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (my_row >= a.T * a.G) return;
+  constexpr int TEAMS = WIDE ? 2 : 1, C = D / 64;          // pairs of columns per lane
+  float m = -INFINITY, l = 0.f;
+  float2 o[C];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float f = mm == -INFINITY ? 1.f : ex2(sm[k] - mm);
-    l = fmaf(f, sl[k], l);
-    o = fmaf(f, so[k][col], o);
+  for (int c = 0; c < C; ++c) o[c] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int i = i0; i <= i1; ++i) {
+    const float2* q = reinterpret_cast<const float2*>(a.part + (((size_t)(i + unit) * TEAMS + w) * p.rows + row) * (D + 2));
+    const float2 ml = __ldcg(q);
+    const float mn = fmaxf(m, ml.x);
+    const float f0 = mn == -INFINITY ? 1.f : ex2(m - mn), f1 = mn == -INFINITY ? 1.f : ex2(ml.x - mn);
+    m = mn;
+    l = fmaf(f1, ml.y, l * f0);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float2 x = __ldcg(q + 1 + 32 * c + lane);
+      o[c].x = fmaf(f1, x.x, o[c].x * f0);
+      o[c].y = fmaf(f1, x.y, o[c].y * f0);
+    }
   }
-  const size_t at = (((size_t)b * a.T + my_row / a.G) * a.Hq + h * a.G + my_row % a.G) * D + col;
-  O[at] = (OT)(l == 0.f ? 0.f : o / l);
+  OT* out = O + (((size_t)b * a.T + my_row / a.G) * a.Hq + h * a.G + my_row % a.G) * D;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const float x = l == 0.f ? 0.f : o[c].x / l, y = l == 0.f ? 0.f : o[c].y / l;
+    if constexpr (sizeof(OT) == 2) *reinterpret_cast<uint32_t*>(out + 64 * c + 2 * lane) = pack_bf16x2(x, y);
+    else *reinterpret_cast<float2*>(out + 64 * c + 2 * lane) = make_float2(x, y);
+  }
 }
 
 }  // namespace hst
