@@ -113,11 +113,17 @@ int stream_blocks(int pairs, int n) {
 bool tree_wide(int R, sk_dtype o) { return R > 128 && o == SK_BF16; }
 int tree_groups(int R, bool wide) { return wide ? (R + 255) / 256 : (R + 127) / 128; }
 
-// Partials: (blocks + units) runs, each of one or two teams' rows.
+// Copies of the rows that share 128 rows of an MMA, to hold the three terms of
+// f32 outputs (two products for 64 rows, one for 32).
+int tree_copies(int R, sk_dtype o) { return o == SK_BF16 || R > 64 ? 1 : R > 32 ? 2 : 4; }
+
+// Partials: (blocks + units) runs of one or two teams', or copies', rows.
 size_t tree_bytes(int pairs, int R, int d) {
   size_t most = 0;
-  for (int wide = 0; wide < (R > 128 ? 2 : 1); ++wide)
-    most = std::max(most, (kNumSMs + (size_t)pairs * tree_groups(R, wide)) * (wide ? 2 : 1));
+  for (const sk_dtype o : {SK_F32, SK_BF16}) {
+    const bool wide = tree_wide(R, o);
+    most = std::max(most, (kNumSMs + (size_t)pairs * tree_groups(R, wide)) * (wide ? 2 : tree_copies(R, o)));
+  }
   return align256(most * std::min(R, 128) * (d + 2) * sizeof(float));
 }
 
@@ -173,33 +179,56 @@ int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, fl
                          : (f ? launch_stream<D, KV_E4M3, true>(p, B, O, pdl, s) : launch_stream<D, KV_E4M3, false>(p, B, O, pdl, s));
 }
 
-// Drafted tokens over a bf16 cache, on tcgen05.
-template <int D, int KT, int NT, bool WIDE, typename OT>
+// Drafted tokens over a bf16 or 8-bit cache, on tcgen05.
+template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT, typename OT>
 int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
-  using SH = TreeShape<D, KT, WIDE>;
+  using SH = TreeShape<D, KT, WIDE, FMT != KV_BF16>;
   TreeParams p;
   p.a = a;
   p.groups = tree_groups(a.T * a.G, WIDE);
   p.rows = std::min(a.T * a.G, 128);
-  const int pairs = B * a.Hkv;
-  const long long tiles = (long long)pairs * p.groups * ((a.n + KT - 1) / KT);
+  p.parts = WIDE ? 2 : COPIES;
+  const int pairs = B * a.Hkv, R = a.T * a.G;
+  const long long units = (long long)pairs * p.groups, tiles = units * ((a.n + KT - 1) / KT);
   const int blocks = (int)std::min((long long)kNumSMs, tiles);
-  CUtensorMap mk, mv;
-  SK_TRY(encode_rows_map(&mk, a.K, (long)pairs * a.Ncap, D, KT));
-  SK_TRY(encode_rows_map(&mv, a.V, (long)pairs * a.Ncap, D, KT));
-  SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE>>(SH::SMEM)));
-  SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE>, dim3(blocks), TR_THREADS, SH::SMEM, s, false, "tree_attend_kernel", p, B,
-                mk, mv));
-  return launch(tree_merge_kernel<D, KT, WIDE, OT>, dim3((a.T * a.G + TREE_MERGE_ROWS - 1) / TREE_MERGE_ROWS, pairs),
-                32 * TREE_MERGE_ROWS, 0, s, true, "tree_merge_kernel", p, O, B,
+  CUtensorMap mk = {}, mv = {};
+  if (FMT == KV_BF16) {
+    SK_TRY(encode_rows_map(&mk, a.K, (long)pairs * a.Ncap, D, KT));
+    SK_TRY(encode_rows_map(&mv, a.V, (long)pairs * a.Ncap, D, KT));
+  }
+  SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT>>(SH::SMEM)));
+  SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT>, dim3(blocks), SH::THREADS, SH::SMEM, s, false,
+                "tree_attend_kernel", p, B, mk, mv));
+  // about blocks / units partials to a row: one warp takes a few, eight take many
+  if (blocks > 6 * units)
+    return launch(tree_merge_kernel<D, KT, WIDE, 8, OT>, dim3(R, pairs), 256, 0, s, true, "tree_merge_kernel", p, O, B, blocks);
+  return launch(tree_merge_kernel<D, KT, WIDE, 1, OT>, dim3((R + 7) / 8, pairs), 256, 0, s, true, "tree_merge_kernel", p, O, B,
                 blocks);
 }
 
-template <int D>
+template <int D, int FMT>
 int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStream_t s) {
-  if (o == SK_F32) return launch_tree<D, 128, 3, false>(a, B, reinterpret_cast<float*>(O), s);
+  const int R = a.T * a.G;
+  if (o == SK_F32) {
+    float* out = reinterpret_cast<float*>(O);
+    if constexpr (FMT == KV_BF16) {
+      const int copies = tree_copies(R, o);
+      return copies == 4   ? launch_tree<D, 128, 3, false, 4, FMT>(a, B, out, s)
+             : copies == 2 ? launch_tree<D, 128, 3, false, 2, FMT>(a, B, out, s)
+                           : launch_tree<D, 128, 3, false, 1, FMT>(a, B, out, s);
+    } else {
+      return R <= 64 ? launch_tree<D, 128, 2, false, 2, FMT>(a, B, out, s) : launch_tree<D, 128, 2, false, 1, FMT>(a, B, out, s);
+    }
+  }
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
-  return tree_wide(a.T * a.G, o) ? launch_tree<D, 64, 1, true>(a, B, out, s) : launch_tree<D, 128, 1, false>(a, B, out, s);
+  return tree_wide(R, o) ? launch_tree<D, 64, 1, true, 1, FMT>(a, B, out, s) : launch_tree<D, 128, 1, false, 1, FMT>(a, B, out, s);
+}
+
+template <int D>
+int tree_attend(const CacheAttendParams& a, sk_dtype kv, int B, void* O, sk_dtype o, cudaStream_t s) {
+  return kv == SK_BF16   ? tree_attend<D, KV_BF16>(a, B, O, o, s)
+         : kv == SK_INT8 ? tree_attend<D, KV_INT8>(a, B, O, o, s)
+                         : tree_attend<D, KV_E4M3>(a, B, O, o, s);
 }
 
 template <int D>
@@ -225,8 +254,8 @@ int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float sca
   if (kv != SK_F32 && p.mode != KEYS_TREE)
     return d == 128 ? stream_attend<128>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s)
                     : stream_attend<64>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s);
-  if (kv == SK_BF16 && p.mode == KEYS_TREE)
-    return d == 128 ? tree_attend<128>(p, B, O, o, s) : tree_attend<64>(p, B, O, o, s);
+  if (q == SK_BF16 && p.mode == KEYS_TREE)
+    return d == 128 ? tree_attend<128>(p, kv, B, O, o, s) : tree_attend<64>(p, kv, B, O, o, s);
   p.splits = rows_splits(pairs, R, p.n);
   SK_TRY(d == 128 ? launch_rows<128>(p, kv, pairs, pdl, s) : launch_rows<64>(p, kv, pairs, pdl, s));
   CacheMergeParams m;

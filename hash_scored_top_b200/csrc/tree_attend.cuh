@@ -1,5 +1,5 @@
-// Attention of T drafted tokens over a bf16 cache on tcgen05 (tree_decode; see
-// cache_attend.cuh for what a token sees).
+// Attention of T drafted tokens over a bf16 or 8-bit cache on tcgen05
+// (tree_decode; see cache_attend.cuh for what a token sees).
 //
 // A KV head's R = T * G query rows are the M side of two products per tile of
 // KT keys: S[128 x KT] = Q . K^T and O[128 x D] += P . V. A cache byte is used by
@@ -24,9 +24,19 @@
 // up to 2^8 lose nothing.
 // The weights enter the second product as NT bf16 terms: one for bf16 outputs
 // (each is off by at most 2^-8, as the output's own rounding is), three (24
-// bits) for f32. Tensor memory holds O and two buffers of S and the third term:
-// 128 + 2 * 192 columns for a team of 128 rows and D = 128; two teams fit with tiles of
-// 64 keys and one term, so f32 outputs of more than 128 rows are taken 128 at a time.
+// bits) for f32. An MMA takes 128 rows, however many there are: with R <= 64 (32)
+// the rows are laid out twice (four times), every copy takes the same weights, and the
+// copies hold different terms, so that three terms take two products (one) instead of
+// three. Tensor memory holds O and two buffers of S and the third term: 128 + 2 * 192
+// columns for a team of 128 rows and D = 128; two teams fit with tiles of 64 keys
+// and one term, so f32 outputs of more than 128 rows are taken 128 at a time.
+//
+// 8-bit caches: warp 8 copies the codes as they lie into a second ring, and four
+// more warps turn them into f16 tiles (exactly), in the layout that TMA gives a
+// bf16 tile, and put the rows' scales beside them. Queries are f16 too, scaled by
+// a power of two per row. A key's scale multiplies its column of S, a value's its
+// weights, which are kept below 2^14 by the largest exponent of a value scale so
+// far, as in stream_attend.cuh; one f16 term (11 bits) for bf16 outputs, two (22) for f32.
 //
 // The list of all (pair, group of rows, tile) is cut into one even run per
 // block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
@@ -47,26 +57,31 @@
 
 namespace hst {
 
-constexpr int TR_THREADS = 320;
 constexpr int TR_MAX_SLOTS = 12;
 constexpr uint32_t TR_SMEM_MAX = 231424;     // dynamic; 1 KB of static shared memory besides
 constexpr int TR_MAX_DRAFT_WORDS = 8;
 
-template <int D, int KT, bool WIDE>
+template <int D, int KT, bool WIDE, bool Q8>
 struct TreeShape {
+  static constexpr int THREADS = Q8 ? 448 : 320;
   static constexpr int QBYTES = 128 * D * 2;               // one Q tile
   static constexpr int SLOT = KT * D * 2;                  // one K or V tile
   static constexpr int QTILES = WIDE ? 2 : 1;
   static constexpr int FIT = ((int)TR_SMEM_MAX - QTILES * QBYTES) / SLOT;
-  static constexpr int SLOTS = FIT < TR_MAX_SLOTS ? FIT : TR_MAX_SLOTS;
-  static constexpr int SMEM = QTILES * QBYTES + SLOTS * SLOT;
-  static_assert(SLOTS >= 6, "the tiles of both buffers and one in flight");
+  static constexpr int SLOTS = Q8 ? 4 : FIT < TR_MAX_SLOTS ? FIT : TR_MAX_SLOTS;
+  // 8 bits: RAWS tiles of codes with their scales, and the scales of four tiles as the softmax reads them
+  static constexpr int RAW = KT * D + KT * 8;
+  static constexpr int RAW_FIT = ((int)TR_SMEM_MAX - QTILES * QBYTES - SLOTS * SLOT - 4 * KT * 8) / RAW;
+  static constexpr int RAWS = !Q8 ? 0 : RAW_FIT < 6 ? RAW_FIT : 6;
+  static constexpr int SMEM = QTILES * QBYTES + SLOTS * SLOT + RAWS * RAW + (Q8 ? 4 * KT * 8 : 0);
+  static_assert(Q8 ? RAWS >= 3 : SLOTS >= 6, "the tiles of both buffers and one in flight");
 };
 
 struct TreeParams {
   CacheAttendParams a;
   int groups;                // groups of 128 (WIDE: 256) rows of a pair
   int rows;                  // rows of a partial: min(R, 128)
+  int parts;                 // partials of a run: teams, or copies of the rows
 };
 
 // Tiles of a sequence's units: its cached and its drafted keys.
@@ -131,9 +146,9 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHi)
       : "memory");
 }
-// f32 accumulators, bf16 operands, M = 128; B is N-major if b_mn.
-__device__ __forceinline__ constexpr uint32_t tree_idesc(int n, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+// f32 accumulators, bf16 (f16) operands, M = 128; B is N-major if b_mn.
+__device__ __forceinline__ constexpr uint32_t tree_idesc(int n, bool b_mn, bool f16 = false) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -171,24 +186,40 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+// Two f32 from shared memory.
+__device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float v;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
   return v;
 }
 
-template <int D, int KT, int NT, bool WIDE>
-__global__ void __launch_bounds__(TR_THREADS, 1)
+// NT terms of the weights in COPIES copies of the rows.
+template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT>
+__global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREADS, 1)
     tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
-  using SH = TreeShape<D, KT, WIDE>;
-  constexpr int NS = SH::SLOTS, ATOMS = D / 64, TEAMS = WIDE ? 2 : 1, TEAM = WIDE ? 128 : 256;
+  constexpr bool Q8 = FMT != KV_BF16;
+  using SH = TreeShape<D, KT, WIDE, Q8>;
+  constexpr int NS = SH::SLOTS, NR = SH::RAWS, ATOMS = D / 64, TEAMS = WIDE ? 2 : 1, TEAM = WIDE ? 128 : 256;
   // tensor memory: O of team w at w * D; buffer sb of its S (and P over it) behind them. Chunk q of 32 keys holds S at
-  // 32 q, then the first two terms of P at 32 q and 32 q + 16, the third at KT + 16 q.
-  constexpr uint32_t SCOLS = NT == 3 ? KT + KT / 2 : KT;
+  // 32 q, then P of the first two products at 32 q and 32 q + 16, of the third at KT + 16 q.
+  constexpr int NP = (NT + COPIES - 1) / COPIES;           // products per tile
+  constexpr uint32_t SCOLS = NP == 3 ? KT + KT / 2 : KT;
+  static_assert(!WIDE || COPIES == 1, "a team has all its rows");
   static_assert(TEAMS * (D + 2 * SCOLS) <= 512, "tensor memory");
   auto s_col = [](int w, int sb) { return (uint32_t)(TEAMS * D) + (uint32_t)(2 * w + sb) * SCOLS; };
   extern __shared__ __align__(1024) unsigned char dyn[];
-  __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 16];
+  __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 16 + (Q8 ? 16 : 0)];
+  __shared__ float vmax_s[4][4];                           // 8 bits: the largest value scale of a tile, by quarters of its rows
   // drafted keys whose V was cleared, by the parity of the segment: they are cleared for a segment while others may
   // still read the last one's
   __shared__ uint32_t bad_s[2][TR_MAX_DRAFT_WORDS];
@@ -199,15 +230,22 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   const uint32_t s0 = smem_u32(dyn), q0 = s0, slots = s0 + SH::QTILES * SH::QBYTES;
   const uint32_t b0 = smem_u32(bars), full = b0, empty = b0 + 8 * TR_MAX_SLOTS, sfull = b0 + 16 * TR_MAX_SLOTS;
   const uint32_t pready = sfull + 32, pvdone = sfull + 64, qready = sfull + 96, halves = sfull + 104, drain = sfull + 112;
+  const uint32_t rfull = sfull + 128, rempty = rfull + 48, scales_in = rempty + 48;      // (8 bits: rings of codes, scales)
+  const uint32_t raws = slots + (uint32_t)(NS * SH::SLOT), scs = raws + (uint32_t)(NR * SH::RAW);
   if (warp == 0) {
     tmem_alloc(smem_u32(&tbase_s), 512u);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, Q8 ? 128 : 1);
       mbar_init(empty + 8 * i, TEAMS);                     // one commit per team
     }
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, 128);
+    }
+    for (int i = 0; i < (Q8 ? 4 : 0); ++i) mbar_init(scales_in + 8 * i, 128);
     for (int i = 0; i < 4; ++i) {                          // team w, buffer sb: 2 w + sb
       mbar_init(sfull + 8 * i, 1);
       mbar_init(pready + 8 * i, TEAM);
@@ -262,27 +300,39 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   if (warp == 8) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
+      constexpr int RING = Q8 ? NR : NS;
+      const uint32_t in = Q8 ? rfull : full, out = Q8 ? rempty : empty;
       int n = 0;
       bool ok = true;
       while (ok && next_segment(seg)) {
         for (int i = seg.ta; i < seg.te && ok; ++i) {
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
-            const int s = n % NS;
-            if (n >= NS && !mbar_wait_bounded(empty + 8 * s, (uint32_t)((n / NS - 1) & 1))) {
+            const int s = n % RING;
+            if (n >= RING && !mbar_wait_bounded(out + 8 * s, (uint32_t)((n / RING - 1) & 1))) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)SH::SLOT);
+            if constexpr (Q8) {
+              // the rows that there are, of codes, and (with K) their scales, an even number for 16 bytes
+              const int rows = min(KT, seg.len + a.T - i * KT), even = (rows + 1) & ~1;
+              const size_t at = (size_t)seg.pair * a.Ncap + (size_t)i * KT;
+              const uint32_t dst = raws + (uint32_t)(s * SH::RAW);
+              mbar_arrive_expect_tx(in + 8 * s, (uint32_t)(rows * D + (kv ? 0 : even * 8)));
+              bulk_copy_g2s(dst, reinterpret_cast<const unsigned char*>(kv ? a.V : a.K) + at * D, (uint32_t)(rows * D), in + 8 * s);
+              if (!kv) bulk_copy_g2s(dst + KT * D, a.scales + 2 * at, (uint32_t)(even * 8), in + 8 * s);
+            } else {
+              mbar_arrive_expect_tx(in + 8 * s, (uint32_t)SH::SLOT);
 #pragma unroll
-            for (int at = 0; at < ATOMS; ++at)
-              tma_load_2d(slot_of(n) + (uint32_t)(at * KT * 128), kv ? &mapV : &mapK, 64 * at, seg.pair * a.Ncap + i * KT,
-                          full + 8 * s);
+              for (int at = 0; at < ATOMS; ++at)
+                tma_load_2d(slot_of(n) + (uint32_t)(at * KT * 128), kv ? &mapV : &mapK, 64 * at, seg.pair * a.Ncap + i * KT,
+                            in + 8 * s);
+            }
           }
         }
       }
       // nothing stays in flight, whatever the others did
-      for (int j = max(0, n - NS); j < n; ++j) mbar_wait_bounded(full + 8 * (j % NS), (uint32_t)((j / NS) & 1));
+      for (int j = max(0, n - RING); j < n; ++j) mbar_wait_bounded(in + 8 * (j % RING), (uint32_t)((j / RING) & 1));
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
@@ -291,7 +341,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     if (elect_one()) {
       bool ok = true;
       int J0 = 0, seg_n = 0;
-      constexpr uint32_t idS = tree_idesc(KT, false), idO = tree_idesc(D, true);
+      constexpr uint32_t idS = tree_idesc(KT, false, Q8), idO = tree_idesc(D, true, Q8);
       auto waits = [&](uint32_t bar, uint32_t parity) {
         ok = ok && mbar_wait_bounded(bar, parity);
         return ok;
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
 #pragma unroll
             for (int s = 0; s < KT / 16; ++s) {
 #pragma unroll
-              for (int k = 0; k < NT; ++k) {
+              for (int k = 0; k < NP; ++k) {
                 const uint32_t at = k < 2 ? 32u * (s >> 1) + 16u * k + 8u * (s & 1) : KT + 8u * s;
                 tc_mma_ts(tb + w * D, ps + at, vs + (uint32_t)(s * 2048 >> 4), idO, s > 0 || k > 0 || i > 0);
               }
@@ -341,12 +391,72 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       tc_commit(drain);                                    // every MMA issued is done before tensor memory is freed
       mbar_wait_bounded(drain, 0u);
     }
+  } else if (Q8 && warp >= 10) {
+    // ---------------------------------------------------------------- 8 bits: codes to f16 tiles
+    if constexpr (Q8) {
+      const int ct = tid - 320;                            // of 128 threads
+      constexpr int CR = D / 16;                           // 16-byte pieces of a row
+      int n = 0, J = 0;
+      bool ok = true;
+      while (ok && next_segment(seg)) {
+        for (int i = seg.ta; i < seg.te && ok; ++i, ++J) {
+          const int rows = min(KT, seg.len + a.T - i * KT);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int r = n % NR, s = n % NS;
+            if (!mbar_wait_bounded(rfull + 8 * r, (uint32_t)((n / NR) & 1)) ||
+                (n >= NS && !mbar_wait_bounded(empty + 8 * s, (uint32_t)((n / NS - 1) & 1)))) {
+              ok = false;
+              break;
+            }
+            const uint32_t src = raws + (uint32_t)(r * SH::RAW), dst = slot_of(n);
+            if (kv == 0) {                                 // the tile's scales, 0 behind the last row
+              float2 x = make_float2(0.f, 0.f);
+              if (ct < rows) {
+                const uint2 u = lds64(src + KT * D + 8u * ct);
+                x = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+              }
+              if (ct < KT) {
+                const uint32_t to = scs + (uint32_t)((J & 3) * KT * 8) + 4u * ct;
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(x.x) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4u * KT), "f"(x.y) : "memory");
+              }
+              float vm = fabsf(x.y);
+              vm = vm < INFINITY ? vm : 0.f;               // a NaN says nothing of the others' size
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(FULL, vm, o));
+              if (lane == 0) vmax_s[J & 3][warp - 10] = vm;
+              mbar_arrive(scales_in + 8 * (J & 3));
+            }
+#pragma unroll 4
+            for (int x = ct; x < KT * CR; x += 128) {
+              const int row = x / CR, c = x % CR;
+              uint4 v = lds128(src + 16u * x);
+              if (row >= rows) v = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t at = dst + (uint32_t)((c >> 2) * KT * 128 + row * 128), k = 2 * (c & 3);
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((k + y) ^ row) & 7) * 16),
+                             "r"(codes_to_f16x2<FMT, false>(w[2 * y])), "r"(codes_to_f16x2<FMT, true>(w[2 * y])),
+                             "r"(codes_to_f16x2<FMT, false>(w[2 * y + 1])), "r"(codes_to_f16x2<FMT, true>(w[2 * y + 1]))
+                             : "memory");
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(full + 8 * s);
+            mbar_arrive(rempty + 8 * r);
+          }
+        }
+      }
+    }
   } else {
     // ---------------------------------------------------------------- softmax
     constexpr int COLS = 64;                               // columns of a tile per thread
     static_assert(WIDE ? KT == COLS : KT == 2 * COLS, "a thread's columns");
     constexpr int OC = WIDE ? D : D / 2;                   // columns of O that it looks after
-    const int hw = warp >> 2, row = tid & 127;             // WIDE: team, else half of the columns; row of its tile
+    constexpr int RC = 128 / COPIES;                       // rows of a copy
+    const int hw = warp >> 2, lrow = tid & 127;            // WIDE: team, else half of the columns; row of its tile
+    const int copy = COPIES == 1 ? 0 : (warp & 3) * 32 / RC, row = COPIES == 1 ? lrow : lrow % RC;
     const int w = WIDE ? hw : 0, chunk0 = WIDE ? 0 : 2 * hw;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tb + lanes + w * D + (WIDE ? 0u : (uint32_t)(hw * OC));
@@ -354,10 +464,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     int J0 = 0, seg_n = 0, exchanges = 0;
     // the other half's value of this row (WIDE: none)
     auto exchange = [&](float x, float& other) -> bool {
-      half_s[exchanges & 1][hw][row] = x;
+      half_s[exchanges & 1][hw][lrow] = x;
       mbar_arrive(halves);
       if (!mbar_wait_bounded(halves, (uint32_t)(exchanges & 1))) return false;
-      other = half_s[exchanges & 1][hw ^ 1][row];
+      other = half_s[exchanges & 1][hw ^ 1][lrow];
       ++exchanges;
       return true;
     };
@@ -365,28 +475,92 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       const int nt = seg.te - seg.ta;
       const int h = seg.pair % a.Hkv;
       const int my_row = (WIDE ? 256 * seg.grp + 128 * w : 128 * seg.grp) + row;      // of the pair's R
-      const bool live = my_row < R;
+      const bool live = my_row < R && copy < NT;
+      // a warp whose rows are all past R (or a copy without a term): their Q and so their S are zero, which as P is zero too. It takes no weights.
+      const bool idle = my_row - lane >= R || copy >= NT;
       const int t = live ? my_row / a.G : 0, g = live ? my_row % a.G : 0;
       uint32_t* bad = bad_s[seg_n & 1];
       const TreeRow vis = {a.mask ? a.mask + ((size_t)seg.b * a.T + t) * a.mask_words : nullptr, t, seg.len, a.T};
       const size_t qrow = ((size_t)seg.b * a.T + t) * a.Hq + h * a.G + g;
-      // ---- Q: WIDE each team its own tile, else the two halves every other chunk
+      // ---- Q: WIDE each team its own tile, else the two halves every other chunk. 8 bits: f16, filled by a power of
+      // two, which the row's scale takes back
+      float row_scale_log2 = a.scale_log2;
       {
         const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D);
-        const uint32_t dst = q0 + (uint32_t)(w * SH::QBYTES) + (uint32_t)row * 128u;
+        const uint32_t dst = q0 + (uint32_t)(w * SH::QBYTES) + (uint32_t)lrow * 128u;
+        float f = 1.f;
+        if constexpr (Q8) {
+          uint32_t mx = 0u;                                // largest exponent field of a bf16
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max((u[k] >> 7) & 0xffu, (u[k] >> 23) & 0xffu));
+          }
+          const int e = max((int)mx - 127, -112);
+          f = pow2i(13 - e);
+          row_scale_log2 = a.scale_log2 * pow2i((e - 13) / 2) * pow2i((e - 13) - (e - 13) / 2);
+        }
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           if (!WIDE && (c & 1) != hw) continue;
-          const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ row) & 7) * 16)),
+          uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (Q8)
+            v = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f), pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
+                           pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f), pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ lrow) & 7) * 16)),
                        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
         }
         if (tid < TR_MAX_DRAFT_WORDS) bad[tid] = 0u;
         fence_proxy_async_shared();
         mbar_arrive(qready);
       }
+      // the rows of V that a product must not meet (done by the first team, whose product with a tile comes first)
+      auto clear_rows = [&](int J, int j0) -> bool {
+        const int n = 2 * J + 1;
+        if (!mbar_wait_bounded(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) return false;
+        const int pos = j0 + lrow;
+        if (lrow < KT && pos >= seg.len) {
+          const uint32_t vr = slot_of(n) + (uint32_t)lrow * 128u;
+          bool clear = pos >= seg.len + a.T;
+          if (!clear) {
+            bool odd = false;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 x = lds128(vr + (uint32_t)((c >> 3) * KT * 128 + ((c ^ lrow) & 7) * 16));
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) odd |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
+            }
+            if (odd) {
+              atomicOr(&bad[(pos - seg.len) >> 5], 1u << ((pos - seg.len) & 31));
+              clear = true;
+            }
+          }
+          if (clear) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (uint32_t)((c >> 3) * KT * 128 + c % 8 * 16)), "r"(0u)
+                           : "memory");
+          }
+        }
+        fence_proxy_async_shared();
+        return true;
+      };
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < nt; ++i) {
+      int E = -127;                                        // 8 bits: weights are times vf = 2^(5 - E) and the value's scale
+      float vf = pow2i(5 - E);
+      for (int i = 0; i < nt && idle; ++i) {
+        const int J = J0 + i, j0 = (seg.ta + i) * KT;
+        float other;
+        if (!mbar_wait_bounded(bar_of(sfull, w, J), par_of(J)) || (!WIDE && !exchange(-INFINITY, other)) ||
+            (!Q8 && hw == 0 && j0 + KT > seg.len && !clear_rows(J, j0))) {
+          ok = false;
+          break;
+        }
+        mbar_arrive(bar_of(pready, w, J));
+      }
+      for (int i = 0; i < nt && !idle; ++i) {
         const int J = J0 + i, j0 = (seg.ta + i) * KT, jc = j0 + 32 * chunk0;
         const bool tail = j0 + KT > seg.len;
         if (!mbar_wait_bounded(bar_of(sfull, w, J), par_of(J))) {
@@ -397,6 +571,25 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         const uint32_t ts = tb + lanes + s_col(w, J & 1);
         uint32_t v[2][32];
         tmem_ld64(ts + 32u * chunk0, v[0], v[1]);
+        int e = E;
+        const uint32_t kss = scs + (uint32_t)((J & 3) * KT * 8) + 128u * chunk0;      // scales of this thread's keys, of their values
+        if constexpr (Q8) {
+          if (!mbar_wait_bounded(scales_in + 8 * (J & 3), (uint32_t)((J >> 2) & 1))) {
+            ok = false;
+            break;
+          }
+          const float vm = fmaxf(fmaxf(vmax_s[J & 3][0], vmax_s[J & 3][1]), fmaxf(vmax_s[J & 3][2], vmax_s[J & 3][3]));
+          e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float x, y;
+              unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])), lds_f32x2(kss + 128u * q + 4u * k)), x, y);
+              v[q][k] = __float_as_uint(x);
+              v[q][k + 1] = __float_as_uint(y);
+            }
+        }
         // ---- the row's maximum
         float mt = -INFINITY;
         if (!tail && a.scale_log2 >= 0.f) {
@@ -410,13 +603,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
             mt = max3(mt, x, y);
           }
-          mt *= a.scale_log2;
+          mt *= row_scale_log2;
         } else {                                           // masked, or an order that the scale turns round
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t see = vis.sees(jc + 32 * q);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * a.scale_log2 : -INFINITY);
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * row_scale_log2 : -INFINITY);
           }
         }
         if constexpr (!WIDE) {
@@ -428,11 +621,17 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           mt = fmaxf(mt, other);
         }
         // (both halves of a row come to the same answer: they have the same m and mt)
-        if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m))) {
+        if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m) || e > E)) {
           const float mn = fmaxf(m, mt);
-          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          float f = mn == -INFINITY ? 1.f : ex2(m - mn);
           m = mn;
           l *= f;
+          if constexpr (Q8) {
+            const float nf = pow2i(5 - e);
+            f *= nf / vf;                                  // a power of two
+            vf = nf;
+            E = e;
+          }
           if (i > 0) {                                     // once the product before has left O at rest
             if (!mbar_wait_bounded(bar_of(pvdone, w, J - 1), par_of(J - 1))) {
               ok = false;
@@ -457,7 +656,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         // ---- weights, over the S that they come from
         auto weights = [&](auto mask_tag) {
           constexpr bool masked = decltype(mask_tag)::value;
-          const uint64_t sc2 = pack_f32x2(a.scale_log2, a.scale_log2), ms2 = pack_f32x2(-ms, -ms);
+          const uint64_t sc2 = pack_f32x2(row_scale_log2, row_scale_log2), ms2 = pack_f32x2(-ms, -ms);
+          [[maybe_unused]] const uint64_t vf2 = pack_f32x2(vf, vf);
           uint64_t sum = 0ull;                             // (0, 0)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -475,7 +675,20 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!((see >> (k + 1)) & 1u)) y = 0.f;
               }
               sum = add_f32x2(sum, pack_f32x2(x, y));
-              t0[k / 2] = pack_bf16x2(x, y);
+              if constexpr (Q8) {
+                unpack_f32x2(mul_f32x2(pack_f32x2(x, y), mul_f32x2(lds_f32x2(kss + 4u * KT + 128u * q + 4u * k), vf2)), x, y);
+                if constexpr (masked) {                    // (0 times a NaN scale)
+                  if (!((see >> k) & 1u)) x = 0.f;
+                  if (!((see >> (k + 1)) & 1u)) y = 0.f;
+                }
+                t0[k / 2] = pack_f16x2(x, y);
+                if constexpr (NT == 2) {
+                  const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&t0[k / 2]));
+                  t1v[k / 2] = pack_f16x2(x - hi.x, y - hi.y);
+                }
+              } else {
+                t0[k / 2] = pack_bf16x2(x, y);
+              }
               if constexpr (NT == 3) {
                 const float x1 = x - bf16lo_to_f32(t0[k / 2]), y1 = y - bf16hi_to_f32(t0[k / 2]);
                 t1v[k / 2] = pack_bf16x2(x1, y1);
@@ -483,10 +696,31 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
               }
             }
             const uint32_t at = ts + 32u * (chunk0 + q);
-            tmem_st16(at, t0);
-            if constexpr (NT == 3) {
+            if constexpr (NT == 1) {
+              tmem_st16(at, t0);
+            } else if constexpr (NT == 2 && COPIES == 1) {
+              tmem_st16(at, t0);
+              tmem_st16(at + 16u, t1v);
+            } else if constexpr (NT == 2) {                // high | low
+#pragma unroll
+              for (int k = 0; k < 16; ++k) t0[k] = copy == 0 ? t0[k] : t1v[k];
+              tmem_st16(at, t0);
+            } else if constexpr (COPIES == 1) {
+              tmem_st16(at, t0);
               tmem_st16(at + 16u, t1v);
               tmem_st16(ts + KT + 16u * (chunk0 + q), t2);
+            } else if constexpr (COPIES == 2) {            // high | middle, then low | nothing
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                t0[k] = copy == 0 ? t0[k] : t1v[k];
+                t2[k] = copy == 0 ? t2[k] : 0u;
+              }
+              tmem_st16(at, t0);
+              tmem_st16(at + 16u, t2);
+            } else {                                       // high | middle | low
+#pragma unroll
+              for (int k = 0; k < 16; ++k) t0[k] = copy == 0 ? t0[k] : copy == 1 ? t1v[k] : t2[k];
+              tmem_st16(at, t0);
             }
           }
           float x, y;
@@ -495,40 +729,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         };
         if (tail) weights(std::true_type{});
         else weights(std::false_type{});
-        // ---- the rows of V that a product must not meet (the first team, whose product with a tile comes first)
-        if (tail && hw == 0) {
-          const int n = 2 * J + 1;
-          if (!mbar_wait_bounded(full + 8 * (n % NS), (uint32_t)((n / NS) & 1))) {
-            ok = false;
-            break;
-          }
-          const int pos = j0 + row;
-          if (row < KT && pos >= seg.len) {
-            const uint32_t vr = slot_of(n) + (uint32_t)row * 128u;
-            bool clear = pos >= seg.len + a.T;
-            if (!clear) {
-              bool odd = false;
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) {
-                const uint4 x = lds128(vr + (uint32_t)((c >> 3) * KT * 128 + ((c ^ row) & 7) * 16));
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  odd |= (u[k] & 0x7f80u) == 0x7f80u || (u[k] & 0x7f800000u) == 0x7f800000u;
-              }
-              if (odd) {
-                atomicOr(&bad[(pos - seg.len) >> 5], 1u << ((pos - seg.len) & 31));
-                clear = true;
-              }
-            }
-            if (clear) {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vr + (uint32_t)((c >> 3) * KT * 128 + c % 8 * 16)), "r"(0u)
-                             : "memory");
-            }
-          }
-          fence_proxy_async_shared();
+        if (!Q8 && tail && hw == 0 && !clear_rows(J, j0)) {
+          ok = false;
+          break;
         }
         tmem_wait_st();
         tc_fence_before_sync();
@@ -550,16 +753,23 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       }
       tc_fence_after_sync();
       // ---- the team's partial of the row
-      float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * TEAMS + w) * p.rows + row) * (D + 2);
+      // (copies hold terms of the same weights: they add up, and the sum of weights is the first one's)
+      float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * p.parts + (WIDE ? w : copy)) * p.rows + row) * (D + 2);
+      if (copy > 0) l = 0.f;
       uint32_t any_bad = 0u;
 #pragma unroll
       for (int k = 0; k < TR_MAX_DRAFT_WORDS; ++k) any_bad |= bad[k];
 #pragma unroll 1
-      for (int q = 0; q < OC / 32; ++q) {
+      for (int q = 0; q < OC / 32 && !idle; ++q) {
         const int col = (WIDE ? 0 : hw * OC) + 32 * q;
         uint32_t o[32];
         tmem_ld32(to + 32u * q, o);
-        if (any_bad != 0u && live) {                       // rare: drafted keys left out of the products
+        if constexpr (Q8) {
+          const float of = 1.f / vf;                       // a power of two
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * of);
+        }
+        if (!Q8 && any_bad != 0u && live && copy == 0) {                       // rare: drafted keys left out of the products
           for (int i = 0; i < a.T; ++i) {
             if (!((bad[i >> 5] >> (i & 31)) & 1u) || !((vis.drafts(i >> 5) >> (i & 31)) & 1u)) continue;
             const size_t kr = ((size_t)seg.pair * a.Ncap + seg.len + i) * D;
@@ -578,7 +788,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           for (int k = 0; k < 32; k += 2) *reinterpret_cast<uint2*>(out + 2 + col + k) = make_uint2(o[k], o[k + 1]);
         }
       }
-      if (row < p.rows && (WIDE || hw == 0)) *reinterpret_cast<float2*>(out) = make_float2(m, l);
+      if (row < p.rows && !idle && (WIDE || hw == 0)) *reinterpret_cast<float2*>(out) = make_float2(m, l);
       tc_fence_before_sync();                              // O has been read before the next segment's products
       ++seg_n;
     }
@@ -591,43 +801,73 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   }
 }
 
-// Joins the rows' partials in order. A warp per row, grid = (ceil(R / 8), pairs).
-constexpr int TREE_MERGE_ROWS = 8;
-
-template <int D, int KT, bool WIDE, typename OT>
-__global__ void __launch_bounds__(32 * TREE_MERGE_ROWS) tree_merge_kernel(const TreeParams p, OT* O, int B, int blocks) {
+// Joins the rows' partials in order: 8 / WPR rows to a block, WPR warps to a row, each taking every WPR-th partial (a few
+// pairs on many blocks leave many partials to a row). grid = (ceil(R WPR / 8), pairs).
+template <int D, int KT, bool WIDE, int WPR, typename OT>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p, OT* O, int B, int blocks) {
+  __shared__ float sm[8], sl[8];
+  __shared__ float2 so[8][D / 2];
   const CacheAttendParams& a = p.a;
-  const int my_row = blockIdx.x * TREE_MERGE_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WPR;
+  const int my_row = blockIdx.x * (8 / WPR) + warp / WPR;
   const int pair = blockIdx.y, b = pair / a.Hkv, h = pair % a.Hkv;
   const int per = tree_tiles<KT>(a, b);
   const StreamRuns runs = tree_runs<KT>(p, B, blocks);
-  const int grp = my_row / (WIDE ? 256 : 128), row = my_row % 128, w = WIDE ? (my_row >> 7) & 1 : 0;
+  const int grp = my_row / (WIDE ? 256 : 128), row = my_row % 128;
+  // a run has one partial of a row, or one for each copy
+  const int k0 = WIDE ? (my_row >> 7) & 1 : 0, kn = WIDE ? 1 : min(p.parts, 3);
   const int unit = pair * p.groups + grp;
   int first = (h * p.groups + grp) * per;                  // the unit's first tile
   for (int i = 0; i < b; ++i) first += a.Hkv * p.groups * tree_tiles<KT>(a, i);
   const int i0 = runs.of(first), i1 = runs.of(first + per - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (my_row >= a.T * a.G) return;
-  constexpr int TEAMS = WIDE ? 2 : 1, C = D / 64;          // pairs of columns per lane
+  constexpr int C = D / 64;                                // pairs of columns per lane
+  const bool live = my_row < a.T * a.G;
   float m = -INFINITY, l = 0.f;
   float2 o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int i = i0; i <= i1; ++i) {
-    const float2* q = reinterpret_cast<const float2*>(a.part + (((size_t)(i + unit) * TEAMS + w) * p.rows + row) * (D + 2));
-    const float2 ml = __ldcg(q);
-    const float mn = fmaxf(m, ml.x);
-    const float f0 = mn == -INFINITY ? 1.f : ex2(m - mn), f1 = mn == -INFINITY ? 1.f : ex2(ml.x - mn);
+  auto add = [&](float pm, float pl, const float2 (&po)[C]) {
+    const float mn = fmaxf(m, pm);
+    const float f0 = mn == -INFINITY ? 1.f : ex2(m - mn), f1 = mn == -INFINITY ? 1.f : ex2(pm - mn);
     m = mn;
-    l = fmaf(f1, ml.y, l * f0);
+    l = fmaf(f1, pl, l * f0);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float2 x = __ldcg(q + 1 + 32 * c + lane);
-      o[c].x = fmaf(f1, x.x, o[c].x * f0);
-      o[c].y = fmaf(f1, x.y, o[c].y * f0);
+      o[c].x = fmaf(f1, po[c].x, o[c].x * f0);
+      o[c].y = fmaf(f1, po[c].y, o[c].y * f0);
+    }
+  };
+  if (live) {
+#pragma unroll 2
+    for (int i = i0 + part; i <= i1; i += WPR) {
+      for (int k = k0; k < k0 + kn; ++k) {
+        const float2* q = reinterpret_cast<const float2*>(a.part + (((size_t)(i + unit) * p.parts + k) * p.rows + row) * (D + 2));
+        const float2 ml = __ldcg(q);
+        float2 x[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = __ldcg(q + 1 + 32 * c + lane);
+        add(ml.x, ml.y, x);
+      }
     }
   }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) so[warp][32 * c + lane] = o[c];
+    __syncthreads();
+    if (part > 0) return;
+    for (int x = 1; x < WPR; ++x) {
+      float2 y[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) y[c] = so[warp + x][32 * c + lane];
+      add(sm[warp + x], sl[warp + x], y);
+    }
+  }
+  if (!live) return;
   OT* out = O + (((size_t)b * a.T + my_row / a.G) * a.Hq + h * a.G + my_row % a.G) * D;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
