@@ -309,6 +309,26 @@ int check_select(const void* Q, sk_dtype q, const void* bsum, int B, int Hq, int
   return SK_OK;
 }
 
+template <int D, typename QT>
+int launch_select(const BlockSelectParams& p, int pairs, int C, size_t smem, cudaStream_t s) {
+  SK_TRY((allow_smem<block_select_kernel<D, QT>>(BSEL_MAX_KEYS * 4)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pairs * C);
+  cfg.blockDim = dim3(BSEL_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, block_select_kernel<D, QT>, p, C);
+  if (e != cudaSuccess) return fail(SK_ERR_CUDA, "block_select_kernel: %s", cudaGetErrorString(e));
+  return check_launch("block_select_kernel");
+}
+
 int select_impl(const void* Q, sk_dtype q, const void* bsum, const int* lens, int B, int Hq, int Hkv, int Ncap, int N,
                 int d, int block, int k, int n_first, int n_last, int* idx, void* ws, cudaStream_t s) {
   BlockSelectParams p;
@@ -325,12 +345,15 @@ int select_impl(const void* Q, sk_dtype q, const void* bsum, const int* lens, in
   p.k = k;
   p.n_first = n_first;
   p.n_last = n_last;
-  const int pairs = B * Hkv, warps = BSCORE_THREADS / 32;
-  const int chunks = std::max(1, std::min((num_blocks(N, block) + warps - 1) / warps, (8 * kNumSMs + pairs - 1) / pairs));
-  auto score = d == 128 ? (q == SK_BF16 ? block_score_kernel<128, __nv_bfloat16> : block_score_kernel<128, float>)
-                        : (q == SK_BF16 ? block_score_kernel<64, __nv_bfloat16> : block_score_kernel<64, float>);
-  SK_TRY(launch(score, dim3(chunks, pairs), BSCORE_THREADS, 0, s, false, "block_score_kernel", p));
-  return launch(block_topk_kernel, dim3(pairs), BTOPK_THREADS, 0, s, true, "block_topk_kernel", p);
+  const int pairs = B * Hkv, most = num_blocks(N, block);
+  const bool on_chip = most <= BSEL_MAX_KEYS;
+  if (on_chip) p.keys = nullptr;
+  // the largest cluster (up to 8) with which every pair still runs at once, no larger than there is work for
+  int C = 1;
+  while (C < 8 && 2 * C * pairs <= kNumSMs && most > 64 * C) C *= 2;
+  const size_t smem = on_chip ? (size_t)most * 4 : 0;
+  return d == 128 ? (q == SK_BF16 ? launch_select<128, __nv_bfloat16>(p, pairs, C, smem, s) : launch_select<128, float>(p, pairs, C, smem, s))
+                  : (q == SK_BF16 ? launch_select<64, __nv_bfloat16>(p, pairs, C, smem, s) : launch_select<64, float>(p, pairs, C, smem, s));
 }
 
 int check_cache_args(const void* Q, sk_dtype q, const void* K, const void* V, sk_dtype kv, const float* scales, int B,
