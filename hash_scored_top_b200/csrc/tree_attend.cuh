@@ -176,6 +176,9 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
   return v;
 }
 
+// The value that a bf16 of x's upper half has: x cut off to 8 bits.
+__device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
 // NT terms of the weights in COPIES copies of the rows.
 template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT>
 __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREADS, 1)
@@ -659,13 +662,13 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
                   const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&t0[k / 2]));
                   t1v[k / 2] = pack_f16x2(x - hi.x, y - hi.y);
                 }
-              } else {
+              } else if constexpr (NT == 1) {
                 t0[k / 2] = pack_bf16x2(x, y);
-              }
-              if constexpr (NT == 3) {
-                const float x1 = x - bf16lo_to_f32(t0[k / 2]), y1 = y - bf16hi_to_f32(t0[k / 2]);
-                t1v[k / 2] = pack_bf16x2(x1, y1);
-                t2[k / 2] = pack_bf16x2(x1 - bf16lo_to_f32(t1v[k / 2]), y1 - bf16hi_to_f32(t1v[k / 2]));
+              } else {                                     // 8 bits cut off, 8 more, the rest rounded: 24 bits
+                const float x1 = x - cut_bf16(x), y1 = y - cut_bf16(y);
+                t0[k / 2] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                t1v[k / 2] = __byte_perm(__float_as_uint(x1), __float_as_uint(y1), 0x7632);
+                t2[k / 2] = pack_bf16x2(x1 - cut_bf16(x1), y1 - cut_bf16(y1));
               }
             }
             const uint32_t at = ts + 32u * (chunk0 + q);
