@@ -80,6 +80,9 @@ int check_rows(const int* starts, int Ncap, int n_begin, int n_count) {
   return SK_OK;
 }
 
+// Positions of a pair at most (their tiles are counted in 32 bits).
+constexpr long long kMaxPositions = 1 << 30;
+
 int check_block(int block) {
   if (block != 16 && block != 32 && block != 64 && block != 128)
     return fail(SK_ERR_UNSUPPORTED, "block=%d: 16, 32, 64 or 128 keys", block);
@@ -303,7 +306,7 @@ int check_select(const void* Q, sk_dtype q, const void* bsum, int B, int Hq, int
   SK_TRY(check_grid(B, Hq, Hkv, d));
   SK_TRY(check_cache(Ncap, N));
   SK_TRY(check_block(block));
-  if (k < 1 || (long long)k * block > INT_MAX) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
+  if (k < 1 || (long long)k * block > kMaxPositions) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
   if (n_first < 0 || n_last < 0 || (long long)n_first + n_last > k)
     return fail(SK_ERR_INVALID_ARG, "n_first=%d and n_last=%d must be >= 0 and at most k=%d together", n_first, n_last, k);
   return SK_OK;
@@ -397,12 +400,12 @@ size_t hst::cache_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int 
     case SK_OP_QUANT_DECODE:
       return N < 1 ? bad : attend_bytes(pairs, G, N, d);
     case SK_OP_QUANT_SPARSE_ATTEND:
-      return k < 1 ? bad : attend_bytes(pairs, G, k, d);
+      return k < 1 || k > kMaxPositions ? bad : attend_bytes(pairs, G, k, d);
     case SK_OP_BLOCK_SELECT:
     case SK_OP_BLOCK_ATTEND:
     case SK_OP_BLOCK_DECODE: {
       if (k < 1 || Ncap < 32 || (block != 16 && block != 32 && block != 64 && block != 128) ||
-          (long long)k * block > INT_MAX)
+          (long long)k * block > kMaxPositions)
         return bad;
       if (op == SK_OP_BLOCK_SELECT) return select_bytes(pairs, Ncap, block);
       const size_t at = attend_bytes(pairs, G, k * block, d);
@@ -432,7 +435,7 @@ int hst::quant_list_check(const void* Q, sk_dtype q, const void* Kq, const void*
   SK_NONNULL(Vq);
   SK_TRY(check_8bit(kv));
   SK_TRY(check_cache_args(Q, q, Kq, Vq, kv, scales, B, Hq, Hkv, Ncap, d, O));
-  if (k < 1) return fail(SK_ERR_INVALID_ARG, "k=%d must be >= 1", k);
+  if (k < 1 || k > kMaxPositions) return fail(SK_ERR_INVALID_ARG, "k=%d must be in [1, 2^30]", k);
   return SK_OK;
 }
 
@@ -452,8 +455,10 @@ extern "C" {
 int quant_append(const void* K_new, const void* V_new, sk_dtype src, long long stride_b, long long stride_h,
                  long long stride_n, const int* starts, const int* lens, int B, int Hkv, int Ncap, int n_begin,
                  int n_count, int d, void* Kq, void* Vq, sk_dtype kv, float* scales, void* stream) {
-  SK_NONNULL(K_new);
-  SK_NONNULL(V_new);
+  if (n_count != 0) {            // (an empty tensor has no address)
+    SK_NONNULL(K_new);
+    SK_NONNULL(V_new);
+  }
   SK_NONNULL(Kq);
   SK_NONNULL(Vq);
   SK_NONNULL(scales);
@@ -501,8 +506,10 @@ int quant_read(const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
   SK_NONNULL(Kq);
   SK_NONNULL(Vq);
   SK_NONNULL(scales);
-  SK_NONNULL(K);
-  SK_NONNULL(V);
+  if (n_count != 0) {            // (an empty tensor has no address)
+    SK_NONNULL(K);
+    SK_NONNULL(V);
+  }
   SK_ALIGNED(Kq, 16);
   SK_ALIGNED(Vq, 16);
   SK_ALIGNED(scales, 16);
@@ -606,7 +613,7 @@ int block_attend(const void* Q, sk_dtype q, const void* K, const void* V, sk_dty
   SK_TRY(check_cache_args(Q, q, K, V, kv, scales, B, Hq, Hkv, Ncap, d, O));
   SK_TRY(check_cache(Ncap, N));
   SK_TRY(check_block(block));
-  if (k < 1 || (long long)k * block > INT_MAX) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
+  if (k < 1 || (long long)k * block > kMaxPositions) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
   SK_TRY(check_ws(ws, ws_bytes, cache_workspace_bytes(SK_OP_BLOCK_ATTEND, B, Hq, Hkv, Ncap, N, d, block, k)));
   return block_attend_impl(Q, q, K, V, kv, scales, lens, idx, B, Hq, Hkv, Ncap, N, d, block, k, scale, O, ws, false,
                            as_stream(stream));

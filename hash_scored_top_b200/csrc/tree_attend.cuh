@@ -21,7 +21,8 @@
 // one after the other: 5100 clocks per 128 keys where the cache's bytes take
 // 2500). The weights are written over the S that they come from. O is rescaled
 // only when a row's maximum has grown by more than 2^8 since the last time: weights
-// up to 2^8 lose nothing.
+// up to 2^8 lose nothing. (8-bit caches: 2^1, so that their f16 weights, below 2^15,
+// go down to 2^-38 of the largest.)
 // The weights enter the second product as NT bf16 terms: one for bf16 outputs
 // (each is off by at most 2^-8, as the output's own rounding is), three (24
 // bits) for f32. An MMA takes 128 rows, however many there are: with R <= 64 (32)
@@ -35,7 +36,7 @@
 // more warps turn them into f16 tiles (exactly), in the layout that TMA gives a
 // bf16 tile, and put the rows' scales beside them. Queries are f16 too, scaled by
 // a power of two per row. A key's scale multiplies its column of S, a value's its
-// weights, which are kept below 2^14 by the largest exponent of a value scale so
+// weights, which are kept below 2^15 by the largest exponent of a value scale so
 // far, as in stream_attend.cuh; one f16 term (11 bits) for bf16 outputs, two (22) for f32.
 //
 // The list of all (pair, group of rows, tile) is cut into one even run per
@@ -523,9 +524,11 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         fence_proxy_async_shared();
         return true;
       };
+      // how far (log2) a row's maximum may outgrow the m that its weights are relative to
+      constexpr float LAZY = Q8 ? 1.f : 8.f;
       float m = -INFINITY, l = 0.f;
-      int E = -127;                                        // 8 bits: weights are times vf = 2^(5 - E) and the value's scale
-      float vf = pow2i(5 - E);
+      int E = -127;                                        // 8 bits: weights are times vf = 2^(13 - E) and the value's scale
+      float vf = pow2i(13 - E);
       for (int i = 0; i < nt && idle; ++i) {
         const int J = J0 + i, j0 = (seg.ta + i) * KT;
         float other;
@@ -597,13 +600,13 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           mt = fmaxf(mt, other);
         }
         // (both halves of a row come to the same answer: they have the same m and mt)
-        if (__any_sync(FULL, mt > m + 8.f || (m == -INFINITY && mt > m) || e > E)) {
+        if (__any_sync(FULL, mt > m + LAZY || (m == -INFINITY && mt > m) || e > E)) {
           const float mn = fmaxf(m, mt);
           float f = mn == -INFINITY ? 1.f : ex2(m - mn);
           m = mn;
           l *= f;
           if constexpr (Q8) {
-            const float nf = pow2i(5 - e);
+            const float nf = pow2i(13 - e);
             f *= nf / vf;                                  // a power of two
             vf = nf;
             E = e;

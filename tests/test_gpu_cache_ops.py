@@ -76,10 +76,10 @@ def poison(K, V, scales, b, rows_):
         scales[b, :, rows_, 0], scales[b, :, rows_, 1] = math.inf, math.nan
 
 
-def hold(O, want, A, S, d, n, out="f32"):
-    """O against the oracle's row by row: arrays [..., d] and S [...]."""
+def hold(O, want, A, S, d, n, out="f32", floor=0.0):
+    """O against the oracle's row by row: arrays [..., d] and S [...]. floor: see test_large_queries_and_keys."""
     O = O.double().cpu().numpy()
-    tol = A * ((2 * (d + 8) * S[..., None] + 2 * (n + 64)) * 2.0**-23 + 2.0**-20)
+    tol = A * ((2 * (d + 8) * S[..., None] + 2 * (n + 64)) * 2.0**-23 + 2.0**-20) + floor
     if out == "bf16":
         tol = tol + 2.0**-8 * (A + np.abs(want))
     bad = np.abs(O - want) > tol
@@ -684,3 +684,119 @@ def test_offsets_past_32_bits(api, lib):
         O.copy_(Ot[:, t])
         same()
     assert status(lib) == 0
+
+
+# ---------------------------------------------------------------- the choice of blocks where it is hard
+def choose(api, Q, bsum, N, block, k, first=0, last=0):
+    B, Hkv = bsum.shape[:2]
+    idx = torch.full((B, Hkv, k), -7, dtype=torch.int32, device=DEV)
+    api.block_select(Q, bsum, N, N, block, first, last, idx)
+    Qd, G = Q.double().cpu().numpy(), Q.shape[1] // Hkv
+    b = bsum.double().cpu().numpy()
+    for i in range(B):
+        for h in range(Hkv):
+            with np.errstate(invalid="ignore"):
+                s = cr.block_scores(Qd[i, h * G:(h + 1) * G], b[i, h])
+            want = cr.select_blocks(s, -(-N // block), k, first, last)
+            assert np.array_equal(idx[i, h].cpu().numpy(), want), (i, h)
+
+
+@pytest.mark.parametrize("N, block, k", [(102400, 16, 500), (1048576, 16, 77), (1048576, 16, 70000), (70016, 16, 4376)])
+def test_block_select_of_many_blocks(api, N, block, k):
+    """More blocks than registers hold, than shared memory holds, and k beyond them all."""
+    g = torch.Generator(device=DEV).manual_seed(k)
+    b = torch.randn(1, 1, N // block, 2, 64, generator=g, device=DEV).sort(3)[0].to(torch.bfloat16)
+    choose(api, query(1, "bf16", 1, 2, 64), b, N, block, k, 1, 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("k", [3, 64, 100, 255])
+def test_block_select_near_ties(api, d, k):
+    """Scores that differ by less than f32 sums can tell, and equal ones: the choice is the exact sums'."""
+    B, Hkv, nb = 2, 2, 256
+    g = torch.Generator().manual_seed(k)
+    base = torch.randn(B, Hkv, 1, 2, d, generator=g).sort(3)[0].expand(B, Hkv, nb, 2, d).to(torch.bfloat16).clone()
+    # the last bit of a few small channels, in some blocks
+    bits = base.view(torch.int16)
+    small = base.float().abs().flatten(3).argsort(-1)[..., :3]
+    flip = torch.randint(0, 2, small.shape, generator=g).to(torch.int16)
+    flat = bits.view(B, Hkv, nb, 2 * d)
+    flat.scatter_(3, small, flat.gather(3, small) ^ flip)
+    choose(api, query(k, "f32", B, Hkv * 3, d), base.to(DEV), 16 * nb, 16, k, 1, 0)
+
+
+def test_block_select_infinite_and_nan(api):
+    """More NaN scores, and more infinite ones, than blocks to choose; and fewer."""
+    g = torch.Generator().manual_seed(5)
+    Q = query(2, "bf16", 1, 4, 64).abs() + 0.1
+    for n_nan, n_inf, k in ((30, 0, 20), (30, 0, 38), (0, 30, 12), (20, 20, 25), (40, 0, 7), (0, 0, 40)):
+        b = torch.randn(1, 1, 40, 2, 64, generator=g).sort(3)[0].to(torch.bfloat16)
+        p = torch.randperm(40, generator=g)
+        b[0, 0, p[:n_nan], 1, 3] = math.nan
+        b[0, 0, p[n_nan:n_nan + n_inf], 1, 5] = math.inf
+        choose(api, Q, b.to(DEV), 640, 16, k)
+    b[..., :] = -math.inf
+    b[0, 0, 7] = 1.0
+    choose(api, Q, b.to(DEV), 640, 16, 5)
+
+
+def test_block_select_large_and_small_numbers(api):
+    """Sums that leave f32, subnormal ones, and zeros."""
+    g = torch.Generator().manual_seed(6)
+    for size in (2.0**120, 2.0**-120, 0.0):
+        b = (torch.randn(1, 1, 100, 2, 64, generator=g).sort(3)[0] * size).to(torch.bfloat16)
+        choose(api, query(3, "bf16", 1, 8, 64), b.to(DEV), 1600, 16, 9)
+        choose(api, (query(4, "bf16", 1, 8, 64).float() * 2.0**60).to(torch.bfloat16), b.to(DEV), 1600, 16, 9)
+
+
+def test_nothing_to_append(api, lib):
+    Kq, Vq, sc = api.empty_quant(1, 1, 64, 64)
+    e = torch.empty(1, 1, 0, 64, device=DEV)
+    api.quant_append(e, e, Kq, Vq, sc)
+    api.quant_read(Kq, Vq, sc, e, e)
+    assert status(lib) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8", "f32"])
+def test_negative_and_zero_scale(api, kv):
+    """softmax(-x) and equal weights are softmaxes too."""
+    B, Hkv, G, d, N, T = 1, 2, 4, 64, 150, 40
+    K, V, sc, Kd, Vd = make_cache(kv, 95, B, Hkv, up(N + T), d)
+    q = "f32" if kv == "f32" else "bf16"
+    Q = query(7, q, B, T, Hkv * G, d)
+    tree = random_tree(1, B, T)
+    bl = torch.arange(3, dtype=torch.int32, device=DEV).expand(B, Hkv, 3).contiguous()
+    for scale in (-0.2, 0.0):
+        O = torch.empty(B, T, Hkv * G, d, device=DEV)
+        api.tree_decode(Q, K, V, N, scale, O, mask=api.tree_mask(tree).to(DEV), scales=sc)
+        want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: list(range(N)) + [N + i for i in range(T) if tree[b, t, i]], scale)
+        hold(O, want, A, np.abs(S), d, N + T)
+        O1 = torch.empty(B, Hkv * G, d, device=DEV)
+        api.block_attend(Q[:, 0].contiguous(), K, V, N, 32, bl, scale, O1, scales=sc)
+        want, A, S = oracle(Q[:, :1], Kd, Vd, lambda b, h, t: slice(0, 96), scale)
+        hold(O1[:, None], want, A, np.abs(S), d, 96)
+
+
+@pytest.mark.parametrize("kv, q", [("bf16", "bf16"), ("int8", "bf16"), ("e4m3", "f32"), ("f32", "f32")])
+def test_large_queries_and_keys(api, kv, q):
+    """Logits of hundreds (one key has all the weight), and queries near the ends of their type.
+
+    Weights of an 8-bit cache are f16 terms of w = x * vs * 2^(13 - E): x = 1 or more for the row's heaviest key, vs a
+    key's value scale and 2^E <= the largest of them. The second term leaves at most half of f16's smallest step,
+    2^-25, of a weight however small, which is 2^-25 * 2^(E - 13) * |code| <= 2^-38 * (largest scale) * 448 of a value:
+    over n keys n * 2^-38 * max |v|, divided by a sum of weights of at least 1. Where the heavy key's value is 0,
+    nothing else of the bound is left.
+    """
+    B, Hkv, G, d, N = 1, 2, 4, 128, 300
+    K, V, sc, Kd, Vd = make_cache(kv, 96, B, Hkv, up(N), d)
+    floor = 0.0 if sc is None else N * 2.0**-38 * 448 * float(sc[..., 1].max())
+    for size, scale in ((30.0, 1.0), (2.0**100, 2.0**-100), (2.0**-110, 2.0**100)):
+        Q = (query(8, "f32", B, 1, Hkv * G, d) * size).to(QT[q])
+        O = torch.empty(B, 1, Hkv * G, d, device=DEV)
+        api.tree_decode(Q, K, V, N - 1, scale, O, scales=sc)
+        want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: slice(0, N), scale)
+        hold(O, want, A, S, d, N, floor=floor)
+        if sc is not None:
+            O1 = torch.empty(B, Hkv * G, d, device=DEV)
+            api.quant_decode(Q[:, 0].contiguous(), K, V, sc, N, scale, O1)
+            hold(O1[:, None], want, A, S, d, N, floor=floor)
