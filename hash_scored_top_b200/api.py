@@ -511,20 +511,27 @@ def _cache_code(t: torch.Tensor, quantised: bool = False) -> int:
     return code
 
 
-def _device(first: torch.Tensor, *others) -> int:
-    """Index of the CUDA device that every tensor given lies on."""
-    i = first.get_device()
-    if i < 0:
+def _addresses(device: int, *tensors):
+    """Addresses of contiguous tensors on one CUDA device (None for None)."""
+    if device < 0:
         raise ValueError("tensors must live on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != i:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device expected")
-    return i
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() != device:
+            raise ValueError(f"tensors on cuda:{device} and {t.device}: one device expected")
+        elif not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        else:
+            out.append(t.data_ptr())
+    return out
 
 
-def _run(device: int, what: str, fn, *args):
-    """fn(*args, the device's current stream) with that device current; raises the library's message."""
-    if device == torch.cuda.current_device():
+def _run(device: int, what: str, *args):
+    """The entry point `what` on the device's current stream, with that device current; raises the library's message."""
+    fn = getattr(_lib.lib, what)
+    if device == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -533,24 +540,21 @@ def _run(device: int, what: str, fn, *args):
         _check(rc, what)
 
 
-def _addr(t):
-    """Address of a contiguous tensor (its device was checked by _device), or None."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+def _need(t, dtype, shape, name):
+    """_want, quick where nothing is wrong."""
+    if t.dtype is not dtype or t.shape != shape:
+        _want(t, dtype, shape, name)
 
 
 def _want_cache(K, V, scales, quantised: bool = False):
     """Checks K, V and their scales; returns the cache's dtype code."""
     code = _cache_code(K, quantised)
-    if V is not None and (V.dtype != K.dtype or V.shape != K.shape):
-        _want(V, K.dtype, K.shape, "V")
+    if V is not None:
+        _need(V, K.dtype, K.shape, "V")
     if code >= SK_INT8:
         if scales is None:
             raise ValueError("scales: a quantised cache needs them")
-        _want(scales, torch.float32, (*K.shape[:3], 2), "scales")
+        _need(scales, torch.float32, (*K.shape[:3], 2), "scales")
     elif scales is not None:
         raise ValueError(f"scales: a {K.dtype} cache has none")
     return code
@@ -558,14 +562,12 @@ def _want_cache(K, V, scales, quantised: bool = False):
 
 def _want_lens(lens, B, name="lens"):
     if lens is not None:
-        _want(lens, torch.int32, (B,), name)
+        _need(lens, torch.int32, (B,), name)
 
 
-def _ws_arg(ws, op, device, *shape):
-    """The workspace's (tensor, address, bytes): the caller's as it is, or one of the size the library asks for."""
-    if ws is None:
-        ws = torch.empty(workspace_bytes(op, *shape), dtype=torch.uint8, device=device)
-    return ws, _addr(ws), ws.numel() * ws.element_size()
+def _ws_arg(ws, op, Q, *shape):
+    """The workspace: the caller's as it is, or one of the size the library asks for."""
+    return ws if ws is not None else torch.empty(workspace_bytes(op, *shape), dtype=torch.uint8, device=Q.device)
 
 
 def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, lens=None):
@@ -574,18 +576,22 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     B, Hkv, Ncap, d = Kq.shape
     n = K_new.shape[2]
     code = _want_cache(Kq, Vq, scales, quantised=True)
-    _want(K_new, K_new.dtype, (B, Hkv, n, d), "K_new")
-    _want(V_new, K_new.dtype, (B, Hkv, n, d), "V_new")
+    _need(K_new, K_new.dtype, (B, Hkv, n, d), "K_new")
+    _need(V_new, K_new.dtype, (B, Hkv, n, d), "V_new")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
-    if V_new.stride() != K_new.stride():
-        raise ValueError(f"V_new: strides {V_new.stride()}, expected K_new's {K_new.stride()}")
-    sb, sh, sn, sd = K_new.stride()
+    strides = K_new.stride()
+    if V_new.stride() != strides:
+        raise ValueError(f"V_new: strides {V_new.stride()}, expected K_new's {strides}")
+    sb, sh, sn, sd = strides
     if sd != 1:
         raise ValueError("K_new, V_new: the last dimension must be contiguous")
-    i = _device(Kq, Vq, scales, K_new, V_new, starts, lens)
-    _run(i, "quant_append", _lib.lib.quant_append, K_new.data_ptr(), V_new.data_ptr(), _dtype_code(K_new), sb, sh, sn,
-         _addr(starts), _addr(lens), B, Hkv, Ncap, n_begin, n, d, _addr(Kq), _addr(Vq), code, _addr(scales))
+    i = Kq.get_device()
+    pk, pv, ps, p_starts, p_lens = _addresses(i, Kq, Vq, scales, starts, lens)
+    if K_new.get_device() != i or V_new.get_device() != i:
+        raise ValueError(f"tensors on {Kq.device}, {K_new.device} and {V_new.device}: one device expected")
+    _run(i, "quant_append", K_new.data_ptr(), V_new.data_ptr(), _dtype_code(K_new), sb, sh, sn, p_starts, p_lens, B, Hkv, Ncap,
+         n_begin, n, d, pk, pv, code, ps)
 
 
 def quant_read(Kq, Vq, scales, K, V, n_begin: int = 0, starts=None, lens=None):
@@ -593,13 +599,13 @@ def quant_read(Kq, Vq, scales, K, V, n_begin: int = 0, starts=None, lens=None):
     B, Hkv, Ncap, d = Kq.shape
     n = K.shape[2]
     code = _want_cache(Kq, Vq, scales, quantised=True)
-    _want(K, K.dtype, (B, Hkv, n, d), "K")
-    _want(V, K.dtype, (B, Hkv, n, d), "V")
+    _need(K, K.dtype, (B, Hkv, n, d), "K")
+    _need(V, K.dtype, (B, Hkv, n, d), "V")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
-    i = _device(Kq, Vq, scales, K, V, starts, lens)
-    _run(i, "quant_read", _lib.lib.quant_read, _addr(Kq), _addr(Vq), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv,
-         Ncap, n_begin, n, d, _addr(K), _addr(V), _dtype_code(K))
+    i = Kq.get_device()
+    pkq, pvq, ps, p_starts, p_lens, pk, pv = _addresses(i, Kq, Vq, scales, starts, lens, K, V)
+    _run(i, "quant_read", pkq, pvq, code, ps, p_starts, p_lens, B, Hkv, Ncap, n_begin, n, d, pk, pv, _dtype_code(K))
 
 
 def quant_decode(Q, Kq, Vq, scales, N: int, scale: float, O, lens=None, ws=None):
@@ -607,13 +613,13 @@ def quant_decode(Q, Kq, Vq, scales, N: int, scale: float, O, lens=None, ws=None)
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
     code = _want_cache(Kq, Vq, scales, quantised=True)
-    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
-    _want(O, torch.float32, (B, Hq, d), "O")
+    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _need(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
-    i = _device(Q, Kq, Vq, scales, O, lens, ws)
-    ws, w, wb = _ws_arg(ws, OP_QUANT_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d)
-    _run(i, "quant_decode", _lib.lib.quant_decode, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code, _addr(scales),
-         _addr(lens), B, Hq, Hkv, Ncap, N, d, scale, _addr(O), w, wb)
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_QUANT_DECODE, Q, B, Hq, Hkv, Ncap, N, d)
+    pq, pk, pv, ps, pl, po, pw = _addresses(i, Q, Kq, Vq, scales, lens, O, ws)
+    _run(i, "quant_decode", pq, _dtype_code(Q), pk, pv, code, ps, pl, B, Hq, Hkv, Ncap, N, d, scale, po, pw, _ws_bytes(ws))
 
 
 def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
@@ -622,13 +628,13 @@ def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
     _, Hkv, Ncap, _ = Kq.shape
     k = idx.shape[-1]
     code = _want_cache(Kq, Vq, scales, quantised=True)
-    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
-    _want(idx, torch.int32, (B, Hkv, k), "idx")
-    _want(O, torch.float32, (B, Hq, d), "O")
-    i = _device(Q, Kq, Vq, scales, idx, O, ws)
-    ws, w, wb = _ws_arg(ws, OP_QUANT_SPARSE_ATTEND, Q.device, B, Hq, Hkv, Ncap, k, d, 0, 0, k)
-    _run(i, "quant_sparse_attend", _lib.lib.quant_sparse_attend, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code,
-         _addr(scales), _addr(idx), B, Hq, Hkv, Ncap, d, k, scale, _addr(O), w, wb)
+    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _need(idx, torch.int32, (B, Hkv, k), "idx")
+    _need(O, torch.float32, (B, Hq, d), "O")
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_QUANT_SPARSE_ATTEND, Q, B, Hq, Hkv, Ncap, k, d, 0, 0, k)
+    pq, pk, pv, ps, pi, po, pw = _addresses(i, Q, Kq, Vq, scales, idx, O, ws)
+    _run(i, "quant_sparse_attend", pq, _dtype_code(Q), pk, pv, code, ps, pi, B, Hq, Hkv, Ncap, d, k, scale, po, pw, _ws_bytes(ws))
 
 
 def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int, tau: float, k: int, scale: float, O,
@@ -637,18 +643,18 @@ def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
     code = _want_cache(Kq, Vq, scales, quantised=True)
-    _want(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
-    _want(R, torch.bfloat16, (L * P, d), "R")
-    _want(ids, torch.uint8, (B, Hkv, Ncap, ids_bytes_per_key(L)), "ids")
-    _want(norms, torch.float16, (B, Hkv, Ncap), "norms")
-    _want(O, torch.float32, (B, Hq, d), "O")
+    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    _need(R, torch.bfloat16, (L * P, d), "R")
+    _need(ids, torch.uint8, (B, Hkv, Ncap, ids_bytes_per_key(L)), "ids")
+    _need(norms, torch.float16, (B, Hkv, Ncap), "norms")
+    _need(O, torch.float32, (B, Hq, d), "O")
     if idx_out is not None:
-        _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
-    i = _device(Q, Kq, Vq, scales, R, ids, norms, O, idx_out, ws)
-    ws, w, wb = _ws_arg(ws, OP_SOCKET_DECODE_QUANT, Q.device, B, Hq, Hkv, Ncap, N, d, L, P, k)
-    _run(i, "socket_decode_quant", _lib.lib.socket_decode_quant, _addr(Q), _dtype_code(Q), _addr(Kq), _addr(Vq), code,
-         _addr(scales), _addr(R), _addr(ids), _addr(norms), B, Hq, Hkv, Ncap, N, d, L, P, tau, k, scale, _addr(O),
-         _addr(idx_out), w, wb)
+        _need(idx_out, torch.int32, (B, Hkv, k), "idx_out")
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_SOCKET_DECODE_QUANT, Q, B, Hq, Hkv, Ncap, N, d, L, P, k)
+    pq, pk, pv, ps, pr, p_ids, pn, po, pi, pw = _addresses(i, Q, Kq, Vq, scales, R, ids, norms, O, idx_out, ws)
+    _run(i, "socket_decode_quant", pq, _dtype_code(Q), pk, pv, code, ps, pr, p_ids, pn, B, Hq, Hkv, Ncap, N, d, L, P, tau, k, scale,
+         po, pi, pw, _ws_bytes(ws))
 
 
 def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None = None, scales=None, starts=None, lens=None):
@@ -656,18 +662,18 @@ def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None =
     B, Hkv, Ncap, d = K.shape
     n_count = Ncap - n_begin if n_count is None else n_count
     code = _want_cache(K, None, scales)
-    _want(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
+    _need(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
-    i = _device(K, scales, bsum, starts, lens)
-    _run(i, "block_summarize", _lib.lib.block_summarize, _addr(K), code, _addr(scales), _addr(starts), _addr(lens), B, Hkv,
-         Ncap, n_begin, n_count, d, block, _addr(bsum))
+    i = K.get_device()
+    pk, ps, p_starts, p_lens, pb = _addresses(i, K, scales, starts, lens, bsum)
+    _run(i, "block_summarize", pk, code, ps, p_starts, p_lens, B, Hkv, Ncap, n_begin, n_count, d, block, pb)
 
 
 def _block_shapes(Q, bsum, Ncap, block):
     B, Hq, d = Q.shape
     Hkv = bsum.shape[1]
-    _want(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
+    _need(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
     return B, Hq, Hkv, d
 
 
@@ -675,12 +681,12 @@ def block_select(Q, bsum, Ncap: int, N: int, block: int, n_first: int, n_last: i
     """The idx.shape[-1] blocks of each pair with the largest bounds: idx [B, Hkv, k] int32, ascending, then -1."""
     B, Hq, Hkv, d = _block_shapes(Q, bsum, Ncap, block)
     k = idx.shape[-1]
-    _want(idx, torch.int32, (B, Hkv, k), "idx")
+    _need(idx, torch.int32, (B, Hkv, k), "idx")
     _want_lens(lens, B)
-    i = _device(Q, bsum, idx, lens, ws)
-    ws, w, wb = _ws_arg(ws, OP_BLOCK_SELECT, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-    _run(i, "block_select", _lib.lib.block_select, _addr(Q), _dtype_code(Q), _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d,
-         block, k, n_first, n_last, _addr(idx), w, wb)
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_BLOCK_SELECT, Q, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    pq, pb, pl, pi, pw = _addresses(i, Q, bsum, lens, idx, ws)
+    _run(i, "block_select", pq, _dtype_code(Q), pb, pl, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, pi, pw, _ws_bytes(ws))
 
 
 def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None, lens=None, ws=None):
@@ -689,14 +695,15 @@ def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None,
     _, Hkv, Ncap, _ = K.shape
     k = idx.shape[-1]
     code = _want_cache(K, V, scales)
-    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
-    _want(idx, torch.int32, (B, Hkv, k), "idx")
-    _want(O, torch.float32, (B, Hq, d), "O")
+    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _need(idx, torch.int32, (B, Hkv, k), "idx")
+    _need(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
-    i = _device(Q, K, V, scales, idx, O, lens, ws)
-    ws, w, wb = _ws_arg(ws, OP_BLOCK_ATTEND, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-    _run(i, "block_attend", _lib.lib.block_attend, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
-         _addr(lens), _addr(idx), B, Hq, Hkv, Ncap, N, d, block, k, scale, _addr(O), w, wb)
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_BLOCK_ATTEND, Q, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    pq, pk, pv, ps, pl, pi, po, pw = _addresses(i, Q, K, V, scales, lens, idx, O, ws)
+    _run(i, "block_attend", pq, _dtype_code(Q), pk, pv, code, ps, pl, pi, B, Hq, Hkv, Ncap, N, d, block, k, scale, po, pw,
+         _ws_bytes(ws))
 
 
 def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last: int, scale: float, O, scales=None, lens=None,
@@ -705,15 +712,16 @@ def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last
     Ncap = K.shape[2]
     B, Hq, Hkv, d = _block_shapes(Q, bsum, Ncap, block)
     code = _want_cache(K, V, scales)
-    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
-    _want(O, torch.float32, (B, Hq, d), "O")
+    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _need(O, torch.float32, (B, Hq, d), "O")
     if idx_out is not None:
-        _want(idx_out, torch.int32, (B, Hkv, k), "idx_out")
+        _need(idx_out, torch.int32, (B, Hkv, k), "idx_out")
     _want_lens(lens, B)
-    i = _device(Q, K, V, scales, bsum, O, lens, idx_out, ws)
-    ws, w, wb = _ws_arg(ws, OP_BLOCK_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, block, 0, k)
-    _run(i, "block_decode", _lib.lib.block_decode, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
-         _addr(bsum), _addr(lens), B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, scale, _addr(O), _addr(idx_out), w, wb)
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_BLOCK_DECODE, Q, B, Hq, Hkv, Ncap, N, d, block, 0, k)
+    pq, pk, pv, ps, pb, pl, po, pi, pw = _addresses(i, Q, K, V, scales, bsum, lens, O, idx_out, ws)
+    _run(i, "block_decode", pq, _dtype_code(Q), pk, pv, code, ps, pb, pl, B, Hq, Hkv, Ncap, N, d, block, k, n_first, n_last, scale,
+         po, pi, pw, _ws_bytes(ws))
 
 
 def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=None, ws=None):
@@ -722,12 +730,13 @@ def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=N
     B, T, Hq, d = Q.shape
     _, Hkv, Ncap, _ = K.shape
     code = _want_cache(K, V, scales)
-    _want(K, K.dtype, (B, Hkv, Ncap, d), "K")
-    _want(O, O.dtype, (B, T, Hq, d), "O")
+    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    _need(O, O.dtype, (B, T, Hq, d), "O")
     if mask is not None:
-        _want(mask, torch.int32, (B, T, -(-T // 32)), "mask")
+        _need(mask, torch.int32, (B, T, -(-T // 32)), "mask")
     _want_lens(lens, B)
-    i = _device(Q, K, V, scales, O, mask, lens, ws)
-    ws, w, wb = _ws_arg(ws, OP_TREE_DECODE, Q.device, B, Hq, Hkv, Ncap, N, d, 0, 0, T)
-    _run(i, "tree_decode", _lib.lib.tree_decode, _addr(Q), _dtype_code(Q), _addr(K), _addr(V), code, _addr(scales),
-         _addr(lens), _addr(mask), B, T, Hq, Hkv, Ncap, N, d, scale, _addr(O), _dtype_code(O), w, wb)
+    i = Q.get_device()
+    ws = _ws_arg(ws, OP_TREE_DECODE, Q, B, Hq, Hkv, Ncap, N, d, 0, 0, T)
+    pq, pk, pv, ps, pl, pm, po, pw = _addresses(i, Q, K, V, scales, lens, mask, O, ws)
+    _run(i, "tree_decode", pq, _dtype_code(Q), pk, pv, code, ps, pl, pm, B, T, Hq, Hkv, Ncap, N, d, scale, po, _dtype_code(O), pw,
+         _ws_bytes(ws))

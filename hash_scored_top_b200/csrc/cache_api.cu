@@ -116,16 +116,18 @@ int stream_blocks(int pairs, int n) {
 bool tree_wide(int R, sk_dtype o) { return R > 128 && o == SK_BF16; }
 int tree_groups(int R, bool wide) { return wide ? (R + 255) / 256 : (R + 127) / 128; }
 
-// Copies of the rows that share 128 rows of an MMA, to hold the three terms of
-// f32 outputs (two products for 64 rows, one for 32).
-int tree_copies(int R, sk_dtype o) { return o == SK_BF16 || R > 64 ? 1 : R > 32 ? 2 : 4; }
+// Copies of the rows that share 128 rows of an MMA, at most. bf16 caches and f32
+// outputs: they hold the three terms of the weights (two products for 64 rows, one
+// for 32). 8-bit caches: two, for the two terms, or, with bf16 outputs, to share a
+// tile's keys, which keeps the softmax threads of all lanes busy.
+int tree_copies(int R) { return R > 64 ? 1 : R > 32 ? 2 : 4; }
 
 // Partials: (blocks + units) runs of one or two teams', or copies', rows.
 size_t tree_bytes(int pairs, int R, int d) {
   size_t most = 0;
   for (const sk_dtype o : {SK_F32, SK_BF16}) {
     const bool wide = tree_wide(R, o);
-    most = std::max(most, (kNumSMs + (size_t)pairs * tree_groups(R, wide)) * (wide ? 2 : tree_copies(R, o)));
+    most = std::max(most, (kNumSMs + (size_t)pairs * tree_groups(R, wide)) * (wide ? 2 : tree_copies(R)));
   }
   return align256(most * std::min(R, 128) * (d + 2) * sizeof(float));
 }
@@ -215,15 +217,17 @@ int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStre
   if (o == SK_F32) {
     float* out = reinterpret_cast<float*>(O);
     if constexpr (FMT == KV_BF16) {
-      const int copies = tree_copies(R, o);
+      const int copies = tree_copies(R);
       return copies == 4   ? launch_tree<D, 128, 3, false, 4, FMT>(a, B, out, s)
              : copies == 2 ? launch_tree<D, 128, 3, false, 2, FMT>(a, B, out, s)
-                           : launch_tree<D, 128, 3, false, 1, FMT>(a, B, out, s);
+                           : launch_tree<D, D == 128 ? 64 : 128, 3, false, 1, FMT>(a, B, out, s);
     } else {
       return R <= 64 ? launch_tree<D, 128, 2, false, 2, FMT>(a, B, out, s) : launch_tree<D, 128, 2, false, 1, FMT>(a, B, out, s);
     }
   }
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(O);
+  if constexpr (FMT != KV_BF16)
+    if (R <= 64) return launch_tree<D, 128, 1, false, 2, FMT>(a, B, out, s);
   return tree_wide(R, o) ? launch_tree<D, 64, 1, true, 1, FMT>(a, B, out, s) : launch_tree<D, 128, 1, false, 1, FMT>(a, B, out, s);
 }
 

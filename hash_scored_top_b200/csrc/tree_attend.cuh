@@ -28,9 +28,11 @@
 // bits) for f32. An MMA takes 128 rows, however many there are: with R <= 64 (32)
 // the rows are laid out twice (four times), every copy takes the same weights, and the
 // copies hold different terms, so that three terms take two products (one) instead of
-// three. Tensor memory holds O and two buffers of S and the third term: 128 + 2 * 192
-// columns for a team of 128 rows and D = 128; two teams fit with tiles of 64 keys
-// and one term, so f32 outputs of more than 128 rows are taken 128 at a time.
+// three. The accumulator of an MMA is cut off, not rounded: over a run of 140 tiles O
+// came out 1.2e-5 off, so f32 outputs add it up in plain arithmetic every 8 tiles (1e-6).
+// Tensor memory holds O, that sum and two buffers of S and the third term (for 128
+// rows and D = 128 with tiles of 64 keys: 128 + 128 + 2 * 96 columns). Two teams fit with tiles
+// of 64 keys and one term, so f32 outputs of more than 128 rows are taken 128 at a time.
 //
 // 8-bit caches: warp 8 copies the codes as they lie into a second ring, and four
 // more warps turn them into f16 tiles (exactly), in the layout that TMA gives a
@@ -180,7 +182,8 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
 // The value that a bf16 of x's upper half has: x cut off to 8 bits.
 __device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
-// NT terms of the weights in COPIES copies of the rows.
+// NT terms of the weights in COPIES copies of the rows. With one term the copies share the keys instead: each takes half
+// of a tile's, with a maximum, a sum and an O of its own, and its weights for the others are 0.
 template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT>
 __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREADS, 1)
     tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
@@ -192,7 +195,11 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
   constexpr int NP = (NT + COPIES - 1) / COPIES;           // products per tile
   constexpr uint32_t SCOLS = NP == 3 ? KT + KT / 2 : KT;
   static_assert(!WIDE || COPIES == 1, "a team has all its rows");
-  static_assert(TEAMS * (D + 2 * SCOLS) <= 512, "tensor memory");
+  // f32 outputs: O is added to a second one, which the MMAs do not touch, after every FLUSH tiles
+  constexpr bool LONG = NT > 1;
+  constexpr uint32_t LCOL = TEAMS * (D + 2 * SCOLS);
+  constexpr int FLUSH = 8;
+  static_assert(LCOL + (LONG ? D : 0) <= 512, "tensor memory");
   auto s_col = [](int w, int sb) { return (uint32_t)(TEAMS * D) + (uint32_t)(2 * w + sb) * SCOLS; };
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 16 + (Q8 ? 16 : 0)];
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
 #pragma unroll
               for (int k = 0; k < NP; ++k) {
                 const uint32_t at = k < 2 ? 32u * (s >> 1) + 16u * k + 8u * (s & 1) : KT + 8u * s;
-                tc_mma_ts(tb + w * D, ps + at, vs + (uint32_t)(s * 2048 >> 4), idO, s > 0 || k > 0 || i > 0);
+                tc_mma_ts(tb + w * D, ps + at, vs + (uint32_t)(s * 2048 >> 4), idO, s > 0 || k > 0 || (LONG ? i % FLUSH != 0 : i > 0));
               }
             }
             tc_commit(bar_of(pvdone, w, J));
@@ -405,19 +412,26 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
               if (lane == 0) vmax_s[J & 3][warp - 10] = vm;
               mbar_arrive(scales_in + 8 * (J & 3));
             }
-#pragma unroll 4
-            for (int x = ct; x < KT * CR; x += 128) {
-              const int row = x / CR, c = x % CR;
-              uint4 v = lds128(src + 16u * x);
-              if (row >= rows) v = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              const uint32_t at = dst + (uint32_t)((c >> 2) * KT * 128 + row * 128), k = 2 * (c & 3);
+            constexpr int PER = KT * CR / 128, AT_ONCE = PER < 8 ? PER : 8;      // pieces of a thread; all read, then all written
+            static_assert(PER % AT_ONCE == 0, "pieces");
+#pragma unroll 1
+            for (int x0 = 0; x0 < PER; x0 += AT_ONCE) {
+              uint4 v[AT_ONCE];
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((k + y) ^ row) & 7) * 16),
-                             "r"(codes_to_f16x2<FMT, false>(w[2 * y])), "r"(codes_to_f16x2<FMT, true>(w[2 * y])),
-                             "r"(codes_to_f16x2<FMT, false>(w[2 * y + 1])), "r"(codes_to_f16x2<FMT, true>(w[2 * y + 1]))
-                             : "memory");
+              for (int x = 0; x < AT_ONCE; ++x) v[x] = lds128(src + 16u * (ct + 128 * (x0 + x)));
+#pragma unroll
+              for (int x = 0; x < AT_ONCE; ++x) {
+                const int piece = ct + 128 * (x0 + x), row = piece / CR, c = piece % CR;
+                const bool on = row < rows;
+                const uint32_t w[4] = {on ? v[x].x : 0u, on ? v[x].y : 0u, on ? v[x].z : 0u, on ? v[x].w : 0u};
+                const uint32_t at = dst + (uint32_t)((c >> 2) * KT * 128 + row * 128), k = 2 * (c & 3);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((k + y) ^ row) & 7) * 16),
+                               "r"(codes_to_f16x2<FMT, false>(w[2 * y])), "r"(codes_to_f16x2<FMT, true>(w[2 * y])),
+                               "r"(codes_to_f16x2<FMT, false>(w[2 * y + 1])), "r"(codes_to_f16x2<FMT, true>(w[2 * y + 1]))
+                               : "memory");
+              }
             }
             fence_proxy_async_shared();
             mbar_arrive(full + 8 * s);
@@ -428,13 +442,15 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    constexpr int COLS = 64;                               // columns of a tile per thread
-    static_assert(WIDE ? KT == COLS : KT == 2 * COLS, "a thread's columns");
+    constexpr bool SPLIT = NT == 1 && COPIES == 2;         // (8 bits only)
+    static_assert(NT > 1 || COPIES == 1 || (SPLIT && Q8), "copies");
+    constexpr int COLS = WIDE ? KT : KT / (SPLIT ? 4 : 2), NQ = COLS / 32;      // columns of a tile per thread
+    static_assert(COLS == 32 || COLS == 64, "a thread's columns");
     constexpr int OC = WIDE ? D : D / 2;                   // columns of O that it looks after
     constexpr int RC = 128 / COPIES;                       // rows of a copy
     const int hw = warp >> 2, lrow = tid & 127;            // WIDE: team, else half of the columns; row of its tile
     const int copy = COPIES == 1 ? 0 : (warp & 3) * 32 / RC, row = COPIES == 1 ? lrow : lrow % RC;
-    const int w = WIDE ? hw : 0, chunk0 = WIDE ? 0 : 2 * hw;
+    const int w = WIDE ? hw : 0, chunk0 = WIDE ? 0 : SPLIT ? 2 * copy + hw : NQ * hw;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tb + lanes + w * D + (WIDE ? 0u : (uint32_t)(hw * OC));
     bool ok = true;
@@ -452,9 +468,9 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
       const int nt = seg.te - seg.ta;
       const int h = seg.pair % a.Hkv;
       const int my_row = (WIDE ? 256 * seg.grp + 128 * w : 128 * seg.grp) + row;      // of the pair's R
-      const bool live = my_row < R && copy < NT;
+      const bool live = my_row < R && (SPLIT || copy < NT);
       // a warp whose rows are all past R (or a copy without a term): their Q and so their S are zero, which as P is zero too. It takes no weights.
-      const bool idle = my_row - lane >= R || copy >= NT;
+      const bool idle = my_row - lane >= R || (!SPLIT && copy >= NT);
       const int t = live ? my_row / a.G : 0, g = live ? my_row % a.G : 0;
       uint32_t* bad = bad_s[seg_n & 1];
       const TreeRow vis = {a.mask ? a.mask + ((size_t)seg.b * a.T + t) * a.mask_words : nullptr, t, seg.len, a.T};
@@ -468,6 +484,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         float f = 1.f;
         if constexpr (Q8) {
           uint32_t mx = 0u;                                // largest exponent field of a bf16
+#pragma unroll
           for (int c = 0; c < D / 8; ++c) {
             const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -548,8 +565,9 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         }
         tc_fence_after_sync();
         const uint32_t ts = tb + lanes + s_col(w, J & 1);
-        uint32_t v[2][32];
-        tmem_ld64(ts + 32u * chunk0, v[0], v[1]);
+        uint32_t v[NQ][32];
+        if constexpr (NQ == 2) tmem_ld64(ts + 32u * chunk0, v[0], v[NQ - 1]);
+        else tmem_ld32(ts + 32u * chunk0, v[0]);
         int e = E;
         const uint32_t kss = scs + (uint32_t)((J & 3) * KT * 8) + 128u * chunk0;      // scales of this thread's keys, of their values
         if constexpr (Q8) {
@@ -560,7 +578,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           const float vm = fmaxf(fmaxf(vmax_s[J & 3][0], vmax_s[J & 3][1]), fmaxf(vmax_s[J & 3][2], vmax_s[J & 3][3]));
           e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float x, y;
@@ -573,7 +591,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         float mt = -INFINITY;
         if (!tail && a.scale_log2 >= 0.f) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < NQ; ++q) {
             float x = __uint_as_float(v[q][0]), y = __uint_as_float(v[q][1]);      // two chains
 #pragma unroll
             for (int k = 2; k < 32; k += 4) {
@@ -585,7 +603,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           mt *= row_scale_log2;
         } else {                                           // masked, or an order that the scale turns round
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < NQ; ++q) {
             const uint32_t see = vis.sees(jc + 32 * q);
 #pragma unroll
             for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * row_scale_log2 : -INFINITY);
@@ -599,6 +617,36 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           }
           mt = fmaxf(mt, other);
         }
+        bool fresh = i == 0;                               // the next product begins an O
+        if constexpr (LONG) {
+          if (i > 0 && i % FLUSH == 0) {
+            if (!mbar_wait_bounded(bar_of(pvdone, w, J - 1), par_of(J - 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            fresh = true;
+#pragma unroll 1
+            for (int q = 0; q < OC / 32; ++q) {
+              uint32_t o[32], x[16], y[16];
+              tmem_ld32(to + 32u * q, o);
+              if (i > FLUSH) {
+                uint32_t z[32];
+                tmem_ld32(to + LCOL + 32u * q, z);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(z[k]));
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                x[k] = o[k];
+                y[k] = o[16 + k];
+              }
+              tmem_st16(to + LCOL + 32u * q, x);
+              tmem_st16(to + LCOL + 32u * q + 16u, y);
+            }
+            tmem_wait_st();
+          }
+        }
         // (both halves of a row come to the same answer: they have the same m and mt)
         if (__any_sync(FULL, mt > m + LAZY || (m == -INFINITY && mt > m) || e > E)) {
           const float mn = fmaxf(m, mt);
@@ -611,24 +659,29 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
             vf = nf;
             E = e;
           }
-          if (i > 0) {                                     // once the product before has left O at rest
-            if (!mbar_wait_bounded(bar_of(pvdone, w, J - 1), par_of(J - 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
+          // O (once the product before has left it at rest) and the long sum
+          auto rescale = [&](uint32_t at) {
 #pragma unroll 1
             for (int q = 0; q < OC / 32; ++q) {
               uint32_t o[32], x[16], y[16];
-              tmem_ld32(to + 32u * q, o);
+              tmem_ld32(at + 32u * q, o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 x[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                 y[k] = __float_as_uint(__uint_as_float(o[16 + k]) * f);
               }
-              tmem_st16(to + 32u * q, x);
-              tmem_st16(to + 32u * q + 16u, y);
+              tmem_st16(at + 32u * q, x);
+              tmem_st16(at + 32u * q + 16u, y);
             }
+          };
+          if (LONG && i >= FLUSH) rescale(to + LCOL);
+          if (!fresh) {
+            if (!mbar_wait_bounded(bar_of(pvdone, w, J - 1), par_of(J - 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            rescale(to);
           }
         }
         const float ms = m == -INFINITY ? 0.f : m;
@@ -639,7 +692,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           [[maybe_unused]] const uint64_t vf2 = pack_f32x2(vf, vf);
           uint64_t sum = 0ull;                             // (0, 0)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < NQ; ++q) {
             uint32_t t0[16];
             [[maybe_unused]] uint32_t t1v[16], t2[16];
             [[maybe_unused]] const uint32_t see = masked ? vis.sees(jc + 32 * q) : 0u;
@@ -677,6 +730,12 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
             const uint32_t at = ts + 32u * (chunk0 + q);
             if constexpr (NT == 1) {
               tmem_st16(at, t0);
+              if constexpr (SPLIT) {
+                uint32_t none[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) none[k] = 0u;
+                tmem_st16(ts + 32u * (chunk0 ^ 2), none);  // the same share of the other copy's keys
+              }
             } else if constexpr (NT == 2 && COPIES == 1) {
               tmem_st16(at, t0);
               tmem_st16(at + 16u, t1v);
@@ -732,9 +791,9 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
       }
       tc_fence_after_sync();
       // ---- the team's partial of the row
-      // (copies hold terms of the same weights: they add up, and the sum of weights is the first one's)
+      // (copies that hold terms of the same weights add up, and the sum of weights is the first one's)
       float* out = a.part + (((size_t)(blockIdx.x + seg.unit) * p.parts + (WIDE ? w : copy)) * p.rows + row) * (D + 2);
-      if (copy > 0) l = 0.f;
+      if (!SPLIT && copy > 0) l = 0.f;
       uint32_t any_bad = 0u;
 #pragma unroll
       for (int k = 0; k < TR_MAX_DRAFT_WORDS; ++k) any_bad |= bad[k];
@@ -743,6 +802,14 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         const int col = (WIDE ? 0 : hw * OC) + 32 * q;
         uint32_t o[32];
         tmem_ld32(to + 32u * q, o);
+        if constexpr (LONG) {
+          if (nt > FLUSH) {
+            uint32_t z[32];
+            tmem_ld32(to + LCOL + 32u * q, z);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(z[k]));
+          }
+        }
         if constexpr (Q8) {
           const float of = 1.f / vf;                       // a power of two
 #pragma unroll
