@@ -422,12 +422,14 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
 #pragma unroll
               for (int x = 0; x < AT_ONCE; ++x) {
                 const int piece = ct + 128 * (x0 + x), row = piece / CR, c = piece % CR;
-                const bool on = row < rows;
-                const uint32_t w[4] = {on ? v[x].x : 0u, on ? v[x].y : 0u, on ? v[x].z : 0u, on ? v[x].w : 0u};
-                const uint32_t at = dst + (uint32_t)((c >> 2) * KT * 128 + row * 128), k = 2 * (c & 3);
+                // pieces c and c + 4 of a row go to the same banks of two atoms: they write their halves in turn
+                const bool on = row < rows, turn = c >> 2;
+                const uint32_t w[4] = {!on ? 0u : turn ? v[x].z : v[x].x, !on ? 0u : turn ? v[x].w : v[x].y,
+                                       !on ? 0u : turn ? v[x].x : v[x].z, !on ? 0u : turn ? v[x].y : v[x].w};
+                const uint32_t at = dst + (uint32_t)((c >> 2) * KT * 128 + row * 128), k = 2 * (c & 3) + turn;
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((k + y) ^ row) & 7) * 16),
+                  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((k ^ y) ^ row) & 7) * 16),
                                "r"(codes_to_f16x2<FMT, false>(w[2 * y])), "r"(codes_to_f16x2<FMT, true>(w[2 * y])),
                                "r"(codes_to_f16x2<FMT, false>(w[2 * y + 1])), "r"(codes_to_f16x2<FMT, true>(w[2 * y + 1]))
                                : "memory");

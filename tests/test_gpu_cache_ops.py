@@ -800,3 +800,48 @@ def test_large_queries_and_keys(api, kv, q):
             O1 = torch.empty(B, Hkv * G, d, device=DEV)
             api.quant_decode(Q[:, 0].contiguous(), K, V, sc, N, scale, O1)
             hold(O1[:, None], want, A, S, d, N, floor=floor)
+
+
+@pytest.mark.parametrize("kv, d, G, T, N, out", [("bf16", 64, 2, 3, 200003, "f32"), ("bf16", 128, 4, 12, 150001, "f32"), ("bf16", 128, 4, 40, 100001, "f32"),
+                                                 ("bf16", 64, 4, 33, 150000, "f32"), ("bf16", 128, 4, 40, 100001, "bf16"), ("int8", 64, 2, 3, 200003, "f32"),
+                                                 ("e4m3", 128, 4, 20, 100001, "f32"), ("int8", 128, 4, 12, 150001, "bf16")])
+def test_long_runs_of_tiles(api, lib, kv, d, G, T, N, out):
+    """Caches long enough that a block takes tens of tiles: the accumulators' changes within a run.
+
+    The bound's chain: f32 outputs add the products of 8 tiles (at most 192 of them) before a plain sum, a run has at
+    most 150 tiles with one sum of weights each beside 64 within a tile, and at most 150 partials are joined: 500 steps.
+    bf16 outputs let a run's products follow one another: 150 tiles of 8.
+    """
+    B, Hkv = 1, 2
+    Ncap = up(N + T)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    K, V = (torch.randn(B, Hkv, Ncap, d, generator=g, device=DEV) for _ in range(2))
+    V *= 1 + torch.arange(Ncap, device=DEV)[:, None] % 7                       # no run like another
+    sc = None
+    if kv == "bf16":
+        K, V = K.to(torch.bfloat16), V.to(torch.bfloat16)
+        Kd, Vd = K.double().cpu().numpy(), V.double().cpu().numpy()
+    else:
+        Kq, Vq, sc = api.empty_quant(B, Hkv, Ncap, d, FMT[kv])
+        api.quant_append(K, V, Kq, Vq, sc)
+        Kr, Vr = torch.empty_like(K), torch.empty_like(V)
+        api.quant_read(Kq, Vq, sc, Kr, Vr)
+        K, V, Kd, Vd = Kq, Vq, Kr.double().cpu().numpy(), Vr.double().cpu().numpy()
+    seen = random_tree(T, B, T)
+    Q = query(T, "bf16", B, T, Hkv * G, d)
+    # logits that rise along the cache: the maximum grows in every run
+    Q[..., 0], ramp = 8.0, torch.linspace(-3, 3, Ncap, device=DEV)
+    if kv == "bf16":
+        K[..., 0] = ramp.to(torch.bfloat16)
+        Kd = K.double().cpu().numpy()
+    O = torch.empty(B, T, Hkv * G, d, dtype=QT[out], device=DEV)
+    api.tree_decode(Q, K, V, N, 0.11, O, mask=api.tree_mask(seen).to(DEV), scales=sc)
+    pick = sorted({0, T // 2, T - 1})                                        # some tokens, all heads
+    want, A, S = oracle(Q[:, pick], Kd, Vd, lambda b, h, t: np.array(list(range(N)) + [N + i for i in range(T) if seen[b, pick[t], i]]), 0.11)
+    hold(O[:, pick], want, A, S, d, 500 if out == "f32" else 1500, out)
+    if sc is not None:
+        O1 = torch.empty(B, Hkv * G, d, device=DEV)
+        api.quant_decode(Q[:, 0].contiguous(), K, V, sc, N, 0.11, O1)
+        want, A, S = oracle(Q[:, :1], Kd, Vd, lambda b, h, t: slice(0, N), 0.11)
+        hold(O1[:, None], want, A, S, d, 500)
+    assert status(lib) == 0
