@@ -492,7 +492,7 @@ int quant_append(const void* K_new, const void* V_new, sk_dtype src, long long s
   p.rows = {starts, lens, n_begin, n_count, Ncap};
   p.Hkv = Hkv;
   p.pairs = B * Hkv;
-  const int per_block = QUANT_THREADS / (2 * (d / 8)) * QUANT_UNROLL;
+  const int per_block = d == 128 ? append_rows<128>() : append_rows<64>();
   auto kern = d == 128 ? (src == SK_BF16 ? (kv == SK_INT8 ? quant_append_kernel<128, __nv_bfloat16, KV_INT8>
                                                          : quant_append_kernel<128, __nv_bfloat16, KV_E4M3>)
                                          : (kv == SK_INT8 ? quant_append_kernel<128, float, KV_INT8>
@@ -533,7 +533,7 @@ int quant_read(const void* Kq, const void* Vq, sk_dtype kv, const float* scales,
   p.rows = {starts, lens, n_begin, n_count, Ncap};
   p.Hkv = Hkv;
   p.pairs = B * Hkv;
-  const int per_block = QUANT_THREADS / (2 * (d / 8)) * QUANT_UNROLL;
+  const int per_block = d == 128 ? read_rows<128>() : read_rows<64>();
   auto kern = d == 128 ? (dst == SK_BF16 ? (kv == SK_INT8 ? quant_read_kernel<128, __nv_bfloat16, KV_INT8>
                                                          : quant_read_kernel<128, __nv_bfloat16, KV_E4M3>)
                                          : (kv == SK_INT8 ? quant_read_kernel<128, float, KV_INT8>

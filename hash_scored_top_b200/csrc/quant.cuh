@@ -10,10 +10,12 @@
 // A row of zeros has s = 0; a row with an infinity or a NaN has s = NaN and
 // zero codes, so that all of it reads back as NaN.
 //
-// Both kernels move each byte once and do a few operations per value, so HBM
-// bounds them. A row is D / 8 lanes of 8 values (16-byte loads of bf16 rows);
-// the lanes of a warp take a K row and its V row side by side, so that the
-// row's two scales leave as one 8-byte store.
+// Both kernels move each byte once, so HBM should bound them; the codes' exact
+// rounding is what quant_append comes near to being bound by instead. When it
+// writes a row is D / 16 lanes of two pieces of 8 values, a half row apart (16-byte
+// loads of bf16 rows, 128 bytes in a row): the scale's arithmetic and the
+// exchanges are shared by 16 values. The lanes of a warp take a K row and its V
+// row side by side, so that the row's two scales leave as one 8-byte store.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -58,11 +60,12 @@ struct Raw8F32 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.f;
   }
+  // with the other piece, of the LPR lanes that share the row
   template <int LPR>
-  __device__ __forceinline__ uint32_t amax() const {     // of the LPR lanes that share the row
+  __device__ __forceinline__ uint32_t amax(const Raw8F32& y) const {
     uint32_t a = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) a = max(a, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(y.x[i]) & 0x7fffffffu));
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(FULL, a, o));
     return a;
@@ -76,9 +79,12 @@ struct Raw8B16 {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = ldg_stream(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  static __device__ __forceinline__ uint32_t two(uint4 w) {
+    return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  }
   template <int LPR>
-  __device__ __forceinline__ uint32_t amax() const {     // two 16-bit maxima at a time
-    uint32_t a = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  __device__ __forceinline__ uint32_t amax(const Raw8B16& y) const {     // two 16-bit maxima at a time
+    uint32_t a = __vmaxu2(two(v), two(y.v));
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) a = __vmaxu2(a, __shfl_xor_sync(FULL, a, o));
     return max(a << 16, a & 0xffff0000u);
@@ -131,7 +137,7 @@ __device__ __forceinline__ int nearest_quotient(float x, float s) {
 // most 127 * 2^-22 (its unit in the last place and the sum's rounding); added to 1.5 * 2^23 it rounds to
 // the integer in the low bits. Where it lies within 2^-15 of a half, the
 // quotient decides. (A division for each value took the kernel 106 us where the bytes
-// of 32768 rows of 8 heads take 31; this takes 36.)
+// of 32768 rows of 8 heads take 31; this takes 46.)
 __device__ __forceinline__ uint2 encode_int8(const float (&x)[8], float s) {
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -209,23 +215,29 @@ struct QuantParams {
 };
 
 constexpr int QUANT_THREADS = 256;
-constexpr int QUANT_UNROLL = 4;      // row pairs in flight per lane group
+constexpr int QUANT_UNROLL = 4;      // row pairs in flight per group of lanes
+
+// Row pairs that a block of quant_append_kernel (quant_read_kernel) takes.
+template <int D>
+__host__ __device__ constexpr int append_rows() { return QUANT_THREADS / (2 * (D / 16)) * QUANT_UNROLL; }
+template <int D>
+__host__ __device__ constexpr int read_rows() { return QUANT_THREADS / (2 * (D / 8)) * QUANT_UNROLL; }
 
 // grid = (chunks of rows, pairs).
 template <int D, typename ST, int FMT>
 __global__ void __launch_bounds__(QUANT_THREADS) quant_append_kernel(const QuantParams p) {
-  constexpr int LPR = D / 8;                         // lanes per row
-  constexpr int RPB = QUANT_THREADS / (2 * LPR);     // row pairs per pass of the block
+  constexpr int LPR = D / 16;                        // lanes per row
+  constexpr int RPB = append_rows<D>() / QUANT_UNROLL;     // row pairs per pass of the block
   const int sub = threadIdx.x % LPR, which = (threadIdx.x / LPR) & 1, slot = threadIdx.x / (2 * LPR);
   const int pair = blockIdx.y, b = pair / p.Hkv, h = pair % p.Hkv;
   const int start = p.rows.start(b), end = p.rows.end(b);
   const ST* src = reinterpret_cast<const ST*>(p.src[which]) + b * p.sb + h * p.sh + 8 * sub;
   const size_t row0 = (size_t)pair * p.rows.Ncap;
-  const int i0 = blockIdx.x * (RPB * QUANT_UNROLL) + slot;
-  typename Raw8Of<ST>::type x[QUANT_UNROLL];
+  const int i0 = blockIdx.x * append_rows<D>() + slot;
+  typename Raw8Of<ST>::type x[QUANT_UNROLL][2];
   bool live[QUANT_UNROLL];
   // (for the whole block) all its rows are there and have a place
-  const int last = (blockIdx.x + 1) * (RPB * QUANT_UNROLL) - 1;
+  const int last = (blockIdx.x + 1) * append_rows<D>() - 1;
   const bool inside = last < p.rows.n_count && start >= 0 && (long long)start + last < end;
 #pragma unroll
   for (int u = 0; u < QUANT_UNROLL; ++u) {
@@ -238,19 +250,25 @@ __global__ void __launch_bounds__(QUANT_THREADS) quant_append_kernel(const Quant
       if (i < p.rows.n_count && !live[u] && (r < 0 || r >= p.rows.Ncap) && (!p.rows.lens || r < __ldg(p.rows.lens + b)))
         atomicOr(&g_error_word, ERR_ROWS);
     }
-    if (live[u]) x[u].load(src + i * p.sn);
-    else x[u].zero();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (live[u]) x[u][k].load(src + i * p.sn + k * (D / 2));
+      else x[u][k].zero();
+    }
   }
 #pragma unroll
   for (int u = 0; u < QUANT_UNROLL; ++u) {
-    const float s = row_scale<FMT>(x[u].template amax<LPR>());
+    const float s = row_scale<FMT>(x[u][0].template amax<LPR>(x[u][1]));
     const float sv = __shfl_xor_sync(FULL, s, LPR);  // the V row's scale, in the K row's lanes
     if (!live[u]) continue;
     const size_t row = row0 + (size_t)(start + i0 + u * RPB);
-    float y[8];
-    x[u].get(y);
-    *reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(p.codes[which]) + row * D + 8 * sub) =
-        encode8<FMT>(y, s);
+    unsigned char* out = reinterpret_cast<unsigned char*>(p.codes[which]) + row * D + 8 * sub;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float y[8];
+      x[u][k].get(y);
+      *reinterpret_cast<uint2*>(out + k * (D / 2)) = encode8<FMT>(y, s);
+    }
     if (which == 0 && sub == 0) *reinterpret_cast<float2*>(p.scales + 2 * row) = make_float2(s, sv);
   }
 }
@@ -258,7 +276,7 @@ __global__ void __launch_bounds__(QUANT_THREADS) quant_append_kernel(const Quant
 template <int D, typename ST, int FMT>
 __global__ void __launch_bounds__(QUANT_THREADS) quant_read_kernel(const QuantParams p) {
   constexpr int LPR = D / 8;
-  constexpr int RPB = QUANT_THREADS / (2 * LPR);
+  constexpr int RPB = read_rows<D>() / QUANT_UNROLL;
   const int sub = threadIdx.x % LPR, which = (threadIdx.x / LPR) & 1, slot = threadIdx.x / (2 * LPR);
   const int pair = blockIdx.y, b = pair / p.Hkv;
   const int start = p.rows.start(b), end = p.rows.end(b);
