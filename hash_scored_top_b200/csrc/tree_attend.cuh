@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         const int J = J0 + i, j0 = (seg.ta + i) * KT;
         float other;
         if (!mbar_wait_bounded(bar_of(sfull, w, J), par_of(J)) || (!WIDE && !exchange(-INFINITY, other)) ||
+            (!WIDE && Q8 && j0 + KT > seg.len && !exchange(0.f, other)) ||
             (!Q8 && hw == 0 && j0 + KT > seg.len && !clear_rows(J, j0))) {
           ok = false;
           break;
@@ -577,7 +578,32 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
             ok = false;
             break;
           }
-          const float vm = fmaxf(fmaxf(vmax_s[J & 3][0], vmax_s[J & 3][1]), fmaxf(vmax_s[J & 3][2], vmax_s[J & 3][3]));
+          float vm = 0.f;
+          if (tail) {                                      // of the values that the row sees: an unseen one may be any size
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const uint32_t see = vis.sees(jc + 32 * q);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float x, y;
+                unpack_f32x2(lds_f32x2(kss + 4u * KT + 128u * q + 4u * k), x, y);
+                x = fabsf(x);
+                y = fabsf(y);
+                if (((see >> k) & 1u) && x < INFINITY) vm = fmaxf(vm, x);
+                if (((see >> (k + 1)) & 1u) && y < INFINITY) vm = fmaxf(vm, y);
+              }
+            }
+            if constexpr (!WIDE) {
+              float other;
+              if (!exchange(vm, other)) {
+                ok = false;
+                break;
+              }
+              vm = fmaxf(vm, other);
+            }
+          } else {
+            vm = fmaxf(fmaxf(vmax_s[J & 3][0], vmax_s[J & 3][1]), fmaxf(vmax_s[J & 3][2], vmax_s[J & 3][3]));
+          }
           e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);
 #pragma unroll
           for (int q = 0; q < NQ; ++q)

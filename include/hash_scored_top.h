@@ -417,6 +417,9 @@ int socket_soft_count_attend(const void* Q, const void* V, sk_dtype kv, const vo
  * a sequence are worked on as far as they lie in [0, Ncap) and, if lens is
  * given, below lens[b]; the other rows of the cache (and of the outputs) stay as
  * they are.
+ * Attention over a quantised cache holds a key's weight times its value's scale
+ * to 22 bits, and to 2^-38 of the largest value scale that the query row sees:
+ * values whose rows are that much smaller than another one's are lost beside it.
  * O is f32 unless said otherwise, its layout as Q's. G = Hq / Hkv <= 8 and
  * B * Hkv <= 65535 in all of them. ws, O and scales must be 16-byte aligned.
  */

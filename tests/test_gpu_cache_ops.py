@@ -485,6 +485,28 @@ def test_tree_decode_chain_and_hidden_drafts(api, kv):
     assert torch.isnan(O[:, 12:]).any(-1).all()
 
 
+@pytest.mark.parametrize("T, G, out", [(20, 1, "bf16"), (20, 4, "bf16"), (20, 8, "bf16"), (40, 8, "bf16"), (20, 4, "f32"), (7, 2, "f32"),
+                                       (30, 5, "f32")])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "e4m3"])
+def test_tree_decode_hidden_drafts_of_any_size(api, kv, T, G, out):
+    """Drafts 2^100 times the others' size do not change what the tokens that do not see them get."""
+    B, Hkv, d, N = 1, 2, 128, 150
+    K, V, sc, Kd, Vd = make_cache(kv, 95, B, Hkv, up(N + T), d)
+    big = slice(N + 1, N + T, 2)                                             # the odd drafts
+    if sc is None:
+        K[:, :, big] *= 2.0**100
+        V[:, :, big] *= 2.0**100
+    else:
+        sc[:, :, big] *= 2.0**100
+    Q = query(8, "bf16", B, T, Hkv * G, d)
+    seen = torch.zeros(B, T, T, dtype=torch.bool)
+    seen[:, :, ::2] = torch.tril(torch.ones(T, T, dtype=torch.bool))[:, ::2]
+    O = torch.empty(B, T, Hkv * G, d, dtype=QT[out], device=DEV)
+    api.tree_decode(Q, K, V, N, 0.1, O, scales=sc, mask=api.tree_mask(seen).to(DEV))
+    want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: list(range(N)) + [N + i for i in range(T) if seen[b, t, i]], 0.1)
+    hold(O, want, A, S, d, N + T, out)
+
+
 def test_tree_of_one_token_is_quant_decode(api):
     B, Hkv, G, d, N = 2, 2, 4, 128, 777
     K, V, sc, Kd, Vd = make_cache("int8", 91, B, Hkv, up(N), d)
