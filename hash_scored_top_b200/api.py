@@ -581,8 +581,9 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
     strides = K_new.stride()
-    if V_new.stride() != strides:
-        raise ValueError(f"V_new: strides {V_new.stride()}, expected K_new's {strides}")
+    if V_new.stride() != strides:         # (that of a dimension of one is arbitrary)
+        if any(x != y and size > 1 for x, y, size in zip(V_new.stride(), strides, K_new.shape)):
+            raise ValueError(f"V_new: strides {V_new.stride()}, expected K_new's {strides}")
     sb, sh, sn, sd = strides
     if sd != 1:
         raise ValueError("K_new, V_new: the last dimension must be contiguous")

@@ -6,9 +6,9 @@
 // q_c > 0 and q_c mn_c otherwise, so the bounds of a group's heads add up to
 // one product of length 2 D:
 //   score_b = T- . mn_b + T+ . mx_b,  T- = sum_h min(q_h, 0), T+ = sum_h max(q_h, 0).
-// The products are summed in f64 and the score rounded once to f32: which
-// block is chosen does not depend on the order of the sum, and equal f32
-// scores go to the lower block.
+// The score is that of the sums in f64, rounded once to f32: which block is
+// chosen does not depend on the order of the sum, and equal f32 scores go to
+// the lower block.
 #pragma once
 
 #include "cache_attend.cuh"
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(BSEL_THREADS) block_select_kernel(const BlockS
   const uint32_t keys0 = smem_u32(keys_s);
   const uint32_t dst = C > 1 ? mapa(keys0, 0) : keys0;
   if (C > 1) cluster_wait();
-  float worst = 0.f;
+  uint32_t worst = 0u;                                     // the largest A's bits: infinity and NaN come above every number
   for (int j0 = jw; j0 < nb; j0 += stride * UNROLL) {
     uint4 v[UNROLL];
 #pragma unroll
@@ -259,16 +259,15 @@ __global__ void __launch_bounds__(BSEL_THREADS) block_select_kernel(const BlockS
     const int j = j0 + u * stride + sub;
     if (piece < 8 && j < nb) {
       const bool forced = j < p.n_first || j >= nb - p.n_last;
-      if (!forced) worst = t[1] <= worst ? worst : t[1];   // (a NaN stays)
+      if (!forced) worst = max(worst, __float_as_uint(t[1]) & 0x7fffffffu);
       const uint32_t key = forced ? 0xffffffffu : ordered_bits(t[0]);
       if (p.keys) p.keys[(size_t)pair * p.NB + j] = key;
       else if (C > 1) st_cluster_u32(dst + 4u * (uint32_t)j, key);
       else keys_s[j] = key;
     }
   }
-  // the largest A of each warp: a positive number's bits order like it, infinity and NaN above
   {
-    const uint32_t bits = __reduce_max_sync(FULL, __float_as_uint(worst) & 0x7fffffffu);
+    const uint32_t bits = __reduce_max_sync(FULL, worst);
     const uint32_t at = smem_u32(&worst_s[rank * BSEL_WARPS + warp]);
     if (lane == 0) {
       if (C > 1) st_cluster_u32(mapa(at, 0), bits);

@@ -67,21 +67,25 @@ int check_grid(int B, int Hq, int Hkv, int d) {
   return SK_OK;
 }
 
+// Rows of a pair at most: a tile's, or a block's, more can be counted in 32 bits.
+constexpr int kMaxRows = INT_MAX - 512;
+// Keys that one call attends to, or writes, per pair at most.
+constexpr int kMaxPositions = 1 << 30;
+
 int check_ncap(int Ncap) {
+  if (Ncap > kMaxRows) return fail(SK_ERR_UNSUPPORTED, "Ncap=%d: at most %d rows per pair", Ncap, kMaxRows);
   if (Ncap < 32 || Ncap % 32) return fail(SK_ERR_INVALID_ARG, "Ncap=%d must be a positive multiple of 32", Ncap);
   return SK_OK;
 }
 
 int check_rows(const int* starts, int Ncap, int n_begin, int n_count) {
   SK_TRY(check_ncap(Ncap));
-  if (n_count < 0) return fail(SK_ERR_INVALID_ARG, "n_count=%d must be >= 0", n_count);
+  if (n_count < 0 || n_count > kMaxPositions)
+    return fail(SK_ERR_INVALID_ARG, "n_count=%d must be in [0, %d]", n_count, kMaxPositions);
   if (starts == nullptr && (n_begin < 0 || (long long)n_begin + n_count > Ncap))
     return fail(SK_ERR_INVALID_ARG, "key range [%d, %d+%d) outside [0, Ncap=%d)", n_begin, n_begin, n_count, Ncap);
   return SK_OK;
 }
-
-// Positions of a pair at most (their tiles are counted in 32 bits).
-constexpr long long kMaxPositions = 1 << 30;
 
 int check_block(int block) {
   if (block != 16 && block != 32 && block != 64 && block != 128)
@@ -308,6 +312,7 @@ int check_select(const void* Q, sk_dtype q, const void* bsum, int B, int Hq, int
   SK_ALIGNED(bsum, 16);
   SK_TRY(check_dtype(q));
   SK_TRY(check_grid(B, Hq, Hkv, d));
+  SK_TRY(check_ncap(Ncap));
   SK_TRY(check_cache(Ncap, N));
   SK_TRY(check_block(block));
   if (k < 1 || (long long)k * block > kMaxPositions) return fail(SK_ERR_INVALID_ARG, "k=%d blocks of %d keys", k, block);
@@ -397,7 +402,8 @@ constexpr int kMaxDrafts = 256;
 // ---------------------------------------------------------------- for api.cu
 size_t hst::cache_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int N, int d, int block, int k) {
   const size_t bad = (size_t)-1;
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 8 || (long long)B * Hkv > 65535 || (d != 64 && d != 128))
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 8 || (long long)B * Hkv > 65535 || (d != 64 && d != 128) ||
+      Ncap > kMaxRows || N > kMaxRows)
     return bad;
   const int pairs = B * Hkv, G = Hq / Hkv;
   switch (op) {
@@ -417,7 +423,7 @@ size_t hst::cache_workspace_bytes(int op, int B, int Hq, int Hkv, int Ncap, int 
       return select_bytes(pairs, Ncap, block) + align256((size_t)pairs * k * 4) + at;
     }
     case SK_OP_TREE_DECODE:
-      if (k < 1 || k > kMaxDrafts || N < 0 || N > INT_MAX - k) return bad;
+      if (k < 1 || k > kMaxDrafts || N < 0 || N > kMaxRows - k) return bad;
       return std::max(attend_bytes(pairs, k * G, N + k, d), tree_bytes(pairs, k * G, d));
     default:
       return bad;

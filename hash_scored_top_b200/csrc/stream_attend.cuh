@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
               async_copy16(dst + 16u * ROW + SH::v_place(n, lane_j), Vp + at + 512 * i);
             }
             if constexpr (!B16)
-              if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + 2 * lane));
+              if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (size_t)(x.row + 2 * lane));
           } else {                                         // rows past the end are not read: zeros
 #pragma unroll
             for (int i = 0; i < CP; ++i) {
@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
               async_copy16(dst + 16u * ROW + SH::v_place(n, lane_j), Vp + from, on ? 16 : 0);
             }
             if constexpr (!B16)
-              if (lane < 8) async_copy16(sdst + 16u * lane, Sp + 2 * (x.row + min(2 * lane, 14)), min(max(8 * (x.cnt - 2 * lane), 0), 16));
+              if (lane < 8)
+                async_copy16(sdst + 16u * lane, Sp + 2 * (size_t)(x.row + min(2 * lane, 14)),
+                             min(max(8 * (x.cnt - 2 * lane), 0), 16));
           }
         }
       }

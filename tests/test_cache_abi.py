@@ -70,6 +70,8 @@ REFUSALS = (
     + [(n, {"n_count": -1}, 1, "n_count") for n in ("quant_append", "quant_read", "block_summarize")]
     + [(n, {"n_begin": 60, "n_count": 5}, 1, "range") for n in ("quant_append", "quant_read", "block_summarize")]
     + [(n, {"n_begin": -1}, 1, "range") for n in ("quant_append", "quant_read", "block_summarize")]
+    + [(n, {"n_count": (1 << 30) + 1, "starts": P}, 1, "n_count") for n in ("quant_append", "quant_read", "block_summarize")]
+    + [(n, {"Ncap": 2**31 - 32}, 2, "rows per pair") for n in GOOD]
     + [(n, {"block": 24}, 2, "block=24") for n in ("block_summarize", "block_select", "block_attend", "block_decode")]
     + [(n, {"k": 0}, 1, "k=0") for n in ("quant_sparse_attend", "block_select", "block_attend", "block_decode")]
     + [(n, {"k": 1 << 28}, 1, "blocks of") for n in ("block_select", "block_attend", "block_decode")]
