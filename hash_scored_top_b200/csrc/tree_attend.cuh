@@ -580,17 +580,13 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
           }
           float vm = 0.f;
           if (tail) {                                      // of the values that the row sees: an unseen one may be any size
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < NQ; ++q) {
-              const uint32_t see = vis.sees(jc + 32 * q);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float x, y;
-                unpack_f32x2(lds_f32x2(kss + 4u * KT + 128u * q + 4u * k), x, y);
-                x = fabsf(x);
-                y = fabsf(y);
-                if (((see >> k) & 1u) && x < INFINITY) vm = fmaxf(vm, x);
-                if (((see >> (k + 1)) & 1u) && y < INFINITY) vm = fmaxf(vm, y);
+              uint32_t see = vis.sees(jc + 32 * q);
+#pragma unroll 4
+              for (int k = 0; k < 32; ++k, see >>= 1) {
+                const float x = fabsf(lds_f32(kss + 4u * KT + 128u * q + 4u * k));
+                if ((see & 1u) && x < INFINITY) vm = fmaxf(vm, x);
               }
             }
             if constexpr (!WIDE) {
