@@ -83,6 +83,9 @@ __device__ __forceinline__ float4 row_quad(const void* base, size_t row, int D, 
 
 constexpr int CACHE_THREADS = 256;
 
+// The simple kernel, for f32 caches and for f32 queries of drafted tokens: a
+// warp per key, every format and order of keys. Bound by its instructions: 2027 us
+// for 102400 int8 keys of 32 pairs, G = 4, which stream_attend_kernel takes 118 for.
 // grid = (splits, R, pairs); warp w takes the split's positions w, w + 8, ...
 // and its lanes the head dimension.
 template <int D, int FMT>

@@ -32,6 +32,9 @@
 //     of a value scale so far, next to the running maximum, and enter as two
 //     f16 terms (22 bits). bf16 caches use bf16 products, weights in three
 //     terms (24 bits).
+// 102400 keys of 32 pairs, D = 128, G = 4: bf16 6.46 TB/s (a copy's rate), int8
+// 6.17, e4m3 5.6 (its conversions to f16); D = 64 8-bit rows 4.4 to 4.9, where the
+// work per byte is the largest. A short list (3103 rows a pair) is bound by latency: 19 us.
 #pragma once
 
 #include "cache_attend.cuh"

@@ -45,6 +45,12 @@
 // block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
 // each side, which tree_merge_kernel joins in order.
 //
+// Four sequences of up to 102400 keys, 8 KV heads of 4 queries, D = 128: 16 tokens with f32
+// outputs 282 us (4.8 TB/s; the tensor pipe 51% busy), 64 tokens with bf16 outputs 377 (the
+// exponentials and the products 50% each); in a loop the GPU's power limit makes that
+// 310 to 330 and 420 to 450. 7 tokens over int8, 32761 keys of 8 pairs: 46 us (the conversion,
+// about 3000 clocks a tile).
+//
 // Drafted keys lie behind the cached ones, in the last tiles. Their S is masked
 // per row. A V row that is not finite must reach only the rows that see it,
 // which a product cannot do (0 * NaN): such rows (and the rows behind the
