@@ -189,9 +189,9 @@ int stream_attend(const CacheAttendParams& p, sk_dtype q, sk_dtype kv, int B, fl
 }
 
 // Drafted tokens over a bf16 or 8-bit cache, on tcgen05.
-template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT, typename OT>
+template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT, bool QF32 = false, typename OT>
 int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
-  using SH = TreeShape<D, KT, WIDE, FMT != KV_BF16>;
+  using SH = TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>;
   TreeParams p;
   p.a = a;
   p.groups = tree_groups(a.T * a.G, WIDE);
@@ -205,8 +205,8 @@ int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
     SK_TRY(encode_rows_map(&mk, a.K, (long)pairs * a.Ncap, D, KT));
     SK_TRY(encode_rows_map(&mv, a.V, (long)pairs * a.Ncap, D, KT));
   }
-  SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT>>(SH::SMEM)));
-  SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT>, dim3(blocks), SH::THREADS, SH::SMEM, s, false,
+  SK_TRY((allow_smem<tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT, QF32>>(SH::SMEM)));
+  SK_TRY(launch(tree_attend_kernel<D, KT, NT, WIDE, COPIES, FMT, QF32>, dim3(blocks), SH::THREADS, SH::SMEM, s, false,
                 "tree_attend_kernel", p, B, mk, mv));
   // about blocks / units partials to a row: one warp takes a few, eight take many
   if (blocks > 6 * units)
@@ -216,8 +216,14 @@ int launch_tree(const CacheAttendParams& a, int B, OT* O, cudaStream_t s) {
 }
 
 template <int D, int FMT>
-int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStream_t s) {
+int tree_attend(const CacheAttendParams& a, sk_dtype q, int B, void* O, sk_dtype o, cudaStream_t s) {
   const int R = a.T * a.G;
+  if constexpr (FMT != KV_BF16) {
+    constexpr int KT = D == 128 ? 64 : 128;
+    if (q == SK_F32)
+      return o == SK_F32 ? launch_tree<D, KT, 2, false, 1, FMT, true>(a, B, reinterpret_cast<float*>(O), s)
+                         : launch_tree<D, KT, 2, false, 1, FMT, true>(a, B, reinterpret_cast<__nv_bfloat16*>(O), s);
+  }
   if (o == SK_F32) {
     float* out = reinterpret_cast<float*>(O);
     if constexpr (FMT == KV_BF16) {
@@ -236,20 +242,10 @@ int tree_attend(const CacheAttendParams& a, int B, void* O, sk_dtype o, cudaStre
 }
 
 template <int D>
-int tree_attend(const CacheAttendParams& a, sk_dtype kv, int B, void* O, sk_dtype o, cudaStream_t s) {
-  return kv == SK_BF16   ? tree_attend<D, KV_BF16>(a, B, O, o, s)
-         : kv == SK_INT8 ? tree_attend<D, KV_INT8>(a, B, O, o, s)
-                         : tree_attend<D, KV_E4M3>(a, B, O, o, s);
-}
-
-template <int D>
-int launch_rows(const CacheAttendParams& p, sk_dtype kv, int pairs, bool pdl, cudaStream_t s) {
-  const dim3 grid(p.splits, p.T * p.G, pairs);
-  auto kern = kv == SK_F32    ? cache_attend_rows_kernel<D, KV_F32>
-              : kv == SK_BF16 ? cache_attend_rows_kernel<D, KV_BF16>
-              : kv == SK_INT8 ? cache_attend_rows_kernel<D, KV_INT8>
-                              : cache_attend_rows_kernel<D, KV_E4M3>;
-  return launch(kern, grid, CACHE_THREADS, 0, s, pdl, "cache_attend_rows_kernel", p);
+int tree_attend(const CacheAttendParams& a, sk_dtype q, sk_dtype kv, int B, void* O, sk_dtype o, cudaStream_t s) {
+  return kv == SK_BF16   ? tree_attend<D, KV_BF16>(a, q, B, O, o, s)
+         : kv == SK_INT8 ? tree_attend<D, KV_INT8>(a, q, B, O, o, s)
+                         : tree_attend<D, KV_E4M3>(a, q, B, O, o, s);
 }
 
 // Attention over the positions that `p` describes (all of it but part, splits
@@ -259,16 +255,16 @@ int attend(CacheAttendParams p, sk_dtype q, sk_dtype kv, int B, int d, float sca
   const int pairs = B * p.Hkv, R = p.T * p.G;
   if ((long long)pairs * ((p.n + 15LL) / 16) > INT_MAX)
     return fail(SK_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of 16 keys");
-  p.q_bf16 = q == SK_BF16;
   p.scale_log2 = scale * kLog2e;
   p.part = reinterpret_cast<float*>(ws);
   if (kv != SK_F32 && p.mode != KEYS_TREE)
     return d == 128 ? stream_attend<128>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s)
                     : stream_attend<64>(p, q, kv, B, reinterpret_cast<float*>(O), pdl, s);
-  if (q == SK_BF16 && p.mode == KEYS_TREE)
-    return d == 128 ? tree_attend<128>(p, kv, B, O, o, s) : tree_attend<64>(p, kv, B, O, o, s);
+  if (kv != SK_F32)
+    return d == 128 ? tree_attend<128>(p, q, kv, B, O, o, s) : tree_attend<64>(p, q, kv, B, O, o, s);
   p.splits = rows_splits(pairs, R, p.n);
-  SK_TRY(d == 128 ? launch_rows<128>(p, kv, pairs, pdl, s) : launch_rows<64>(p, kv, pairs, pdl, s));
+  SK_TRY(launch(d == 128 ? cache_attend_rows_kernel<128> : cache_attend_rows_kernel<64>, dim3(p.splits, R, pairs), CACHE_THREADS, 0,
+                s, pdl, "cache_attend_rows_kernel", p));
   CacheMergeParams m;
   m.part = p.part;
   m.O = O;

@@ -35,7 +35,6 @@ struct CacheAttendParams {
   int Hq, Hkv, T, G, Ncap, N, k, block, mask_words;
   int n;                     // positions (an upper bound of a pair's)
   int mode;                  // KeyMode
-  int q_bf16;
   int splits;
   float scale_log2;          // scale * log2(e)
 };
@@ -44,9 +43,8 @@ __device__ __forceinline__ int seq_len(const int* lens, int b, int N) {
   return lens ? min(max(__ldg(lens + b), 0), N) : N;
 }
 
-// What position j of a pair is: its cache row, or -1 when it is not seen.
+// What position j of a pair is (but for KEYS_ALL): its cache row, or -1 when it is not seen.
 __device__ __forceinline__ int key_row(const CacheAttendParams& p, int pair, int b, int t, int len, int j) {
-  if (p.mode == KEYS_ALL) return j < len ? j : -1;
   if (p.mode == KEYS_LISTED) {
     const int r = __ldg(p.idx + (size_t)pair * p.k + j);
     return r >= 0 && r < p.Ncap ? r : -1;
@@ -64,31 +62,23 @@ __device__ __forceinline__ int key_row(const CacheAttendParams& p, int pair, int
   return sees ? j : -1;
 }
 
-// Values 4q .. 4q + 3 of a row, as stored (8-bit codes without their scale).
+// Values 4q .. 4q + 3 of a row of f32 or bf16.
 template <int FMT>
 __device__ __forceinline__ float4 row_quad(const void* base, size_t row, int D, int q) {
   const size_t e = row * D + 4 * q;
   if constexpr (FMT == KV_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + e);
-  if constexpr (FMT == KV_BF16) {
-    const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(base) + e);
-    return make_float4(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y), bf16hi_to_f32(w.y));
-  }
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const unsigned char*>(base) + e);
-  if constexpr (FMT == KV_INT8)
-    return make_float4((float)(signed char)(w & 255u), (float)(signed char)((w >> 8) & 255u),
-                       (float)(signed char)((w >> 16) & 255u), (float)(signed char)(w >> 24));
-  const float2 a = e4m3x2_to_f32(w & 0xffffu), b = e4m3x2_to_f32(w >> 16);
-  return make_float4(a.x, a.y, b.x, b.y);
+  const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(base) + e);
+  return make_float4(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y), bf16hi_to_f32(w.y));
 }
 
 constexpr int CACHE_THREADS = 256;
 
-// The simple kernel, for f32 caches and for f32 queries of drafted tokens: a
-// warp per key, every format and order of keys. Bound by its instructions: 2027 us
-// for 102400 int8 keys of 32 pairs, G = 4, which stream_attend_kernel takes 118 for.
+// The simple kernel, for f32 caches: a warp per key. Bound by its instructions
+// (an int8 form of it took 2027 us for 102400 keys of 32 pairs, G = 4, which
+// stream_attend_kernel takes 118 for).
 // grid = (splits, R, pairs); warp w takes the split's positions w, w + 8, ...
 // and its lanes the head dimension.
-template <int D, int FMT>
+template <int D>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_attend_rows_kernel(const CacheAttendParams p) {
   constexpr int NW = CACHE_THREADS / 32, QL = D / 4;      // QL lanes hold a row (4 values each)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -100,7 +90,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_attend_rows_kernel(const 
   const bool on = lane < QL;
   if (on) {
     const size_t row0 = ((size_t)b * p.T + t) * p.Hq + head;
-    const float4 v = p.q_bf16 ? row_quad<KV_BF16>(p.Q, row0, D, lane) : row_quad<KV_F32>(p.Q, row0, D, lane);
+    const float4 v = row_quad<KV_F32>(p.Q, row0, D, lane);
     q[0] = v.x * p.scale_log2;
     q[1] = v.y * p.scale_log2;
     q[2] = v.z * p.scale_log2;
@@ -113,28 +103,21 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_attend_rows_kernel(const 
   for (int j = j0 + warp; j < j1; j += NW) {
     const int r = key_row(p, pair, b, t, len, j);
     if (r < 0) continue;
-    float ks = 1.f, vs = 1.f;
-    if constexpr (FMT == KV_INT8 || FMT == KV_E4M3) {
-      const float2 s2 = __ldg(reinterpret_cast<const float2*>(p.scales) + base + r);
-      ks = s2.x;
-      vs = s2.y;
-    }
     float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
     if (on) {
-      kv = row_quad<FMT>(p.K, base + r, D, lane);
-      vv = row_quad<FMT>(p.V, base + r, D, lane);
+      kv = row_quad<KV_F32>(p.K, base + r, D, lane);
+      vv = row_quad<KV_F32>(p.V, base + r, D, lane);
     }
-    float s = warp_sum(fmaf(q[0], kv.x, fmaf(q[1], kv.y, fmaf(q[2], kv.z, q[3] * kv.w)))) * ks;
+    float s = warp_sum(fmaf(q[0], kv.x, fmaf(q[1], kv.y, fmaf(q[2], kv.z, q[3] * kv.w))));
     const float mn = fmaxf(m, s);
     const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
     const float pr = s == -INFINITY ? 0.f : exp2f(s - mn);    // a NaN logit stays one
     m = mn;
     l = fmaf(l, al, pr);
-    const float w = pr * vs;
-    o[0] = fmaf(o[0], al, w * vv.x);
-    o[1] = fmaf(o[1], al, w * vv.y);
-    o[2] = fmaf(o[2], al, w * vv.z);
-    o[3] = fmaf(o[3], al, w * vv.w);
+    o[0] = fmaf(o[0], al, pr * vv.x);
+    o[1] = fmaf(o[1], al, pr * vv.y);
+    o[2] = fmaf(o[2], al, pr * vv.z);
+    o[3] = fmaf(o[3], al, pr * vv.w);
   }
   __shared__ float sm[NW], sl[NW], so[NW][D];
   if (lane == 0) {

@@ -40,6 +40,8 @@
 // a power of two per row. A key's scale multiplies its column of S, a value's its
 // weights, which are kept below 2^15 by the largest exponent of a value scale so
 // far, as in stream_attend.cuh; one f16 term (11 bits) for bf16 outputs, two (22) for f32.
+// f32 queries are two f16 tiles, high and low parts, whose products with K add up in S
+// (with D = 128 over tiles of 64 keys, to make room).
 //
 // The list of all (pair, group of rows, tile) is cut into one even run per
 // block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
@@ -70,12 +72,12 @@ constexpr int TR_MAX_SLOTS = 12;
 constexpr uint32_t TR_SMEM_MAX = 231424;     // dynamic; 1 KB of static shared memory besides
 constexpr int TR_MAX_DRAFT_WORDS = 8;
 
-template <int D, int KT, bool WIDE, bool Q8>
+template <int D, int KT, bool WIDE, bool Q8, bool QF32 = false>
 struct TreeShape {
   static constexpr int THREADS = Q8 ? 448 : 320;
   static constexpr int QBYTES = 128 * D * 2;               // one Q tile
   static constexpr int SLOT = KT * D * 2;                  // one K or V tile
-  static constexpr int QTILES = WIDE ? 2 : 1;
+  static constexpr int QTILES = WIDE || QF32 ? 2 : 1;     // f32 queries: high and low parts
   static constexpr int FIT = ((int)TR_SMEM_MAX - QTILES * QBYTES) / SLOT;
   static constexpr int SLOTS = Q8 ? 4 : FIT < TR_MAX_SLOTS ? FIT : TR_MAX_SLOTS;
   // 8 bits: RAWS tiles of codes with their scales, and the scales of four tiles as the softmax reads them
@@ -190,11 +192,12 @@ __device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(__fl
 
 // NT terms of the weights in COPIES copies of the rows. With one term the copies share the keys instead: each takes half
 // of a tile's, with a maximum, a sum and an O of its own, and its weights for the others are 0.
-template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT>
-__global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREADS, 1)
+template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT, bool QF32 = false>
+__global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::THREADS, 1)
     tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
   constexpr bool Q8 = FMT != KV_BF16;
-  using SH = TreeShape<D, KT, WIDE, Q8>;
+  using SH = TreeShape<D, KT, WIDE, Q8, QF32>;
+  static_assert(!QF32 || (Q8 && !WIDE), "f32 queries: 8-bit caches");
   constexpr int NS = SH::SLOTS, NR = SH::RAWS, ATOMS = D / 64, TEAMS = WIDE ? 2 : 1, TEAM = WIDE ? 128 : 256;
   // tensor memory: O of team w at w * D; buffer sb of its S (and P over it) behind them. Chunk q of 32 keys holds S at
   // 32 q, then P of the first two products at 32 q and 32 q + 16, of the third at KT + 16 q.
@@ -345,6 +348,12 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
         for (int s = 0; s < D / 16; ++s)
           tc_mma_ss(sd, qs + (uint32_t)(((s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
                     ks + (uint32_t)(((s >> 2) * KT * 128 + (s & 3) * 32) >> 4), idS, s > 0);
+        if constexpr (QF32) {                              // + the low parts' product
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            tc_mma_ss(sd, qs + (uint32_t)((SH::QBYTES + (s >> 2) * 128 * 128 + (s & 3) * 32) >> 4),
+                      ks + (uint32_t)(((s >> 2) * KT * 128 + (s & 3) * 32) >> 4), idS, true);
+        }
         tc_commit(bar_of(sfull, w, J));
         tc_commit(empty + 8 * (n % NS));
       };
@@ -487,31 +496,61 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16>::THREAD
       // two, which the row's scale takes back
       float row_scale_log2 = a.scale_log2;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D);
         const uint32_t dst = q0 + (uint32_t)(w * SH::QBYTES) + (uint32_t)lrow * 128u;
-        float f = 1.f;
-        if constexpr (Q8) {
-          uint32_t mx = 0u;                                // largest exponent field of a bf16
+        auto put = [&](uint32_t tile, int c, uint4 v) {
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ lrow) & 7) * 16)),
+                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        };
+        if constexpr (QF32) {
+          const float* src = reinterpret_cast<const float*>(a.Q) + qrow * D;
+          uint32_t mx = 0u;                                // the largest magnitude's bits
+#pragma unroll 4
+          for (int c = 0; c < D / 4; ++c) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+            mx = max(max(mx, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu)), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+          }
+          const int e = max((int)(mx >> 23) - 127, -112);
+          const float f = pow2i(13 - e);
+          row_scale_log2 = a.scale_log2 * pow2i((e - 13) / 2) * pow2i((e - 13) - (e - 13) / 2);
+#pragma unroll 2
+          for (int c = hw; c < D / 8; c += 2) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (live) load8(src + 8 * c, x);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              hi[k] = pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
+              const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+              lo[k] = pack_f16x2(x[2 * k] * f - h2.x, x[2 * k + 1] * f - h2.y);
+            }
+            put(dst, c, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            put(dst + SH::QBYTES, c, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          }
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.Q) + qrow * D);
+          float f = 1.f;
+          if constexpr (Q8) {
+            uint32_t mx = 0u;                              // largest exponent field of a bf16
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx = max(mx, max((u[k] >> 7) & 0xffu, (u[k] >> 23) & 0xffu));
+            }
+            const int e = max((int)mx - 127, -112);
+            f = pow2i(13 - e);
+            row_scale_log2 = a.scale_log2 * pow2i((e - 13) / 2) * pow2i((e - 13) - (e - 13) / 2);
+          }
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx = max(mx, max((u[k] >> 7) & 0xffu, (u[k] >> 23) & 0xffu));
+            if (!WIDE && (c & 1) != hw) continue;
+            uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (Q8)
+              v = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f), pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
+                             pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f), pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
+            put(dst, c, v);
           }
-          const int e = max((int)mx - 127, -112);
-          f = pow2i(13 - e);
-          row_scale_log2 = a.scale_log2 * pow2i((e - 13) / 2) * pow2i((e - 13) - (e - 13) / 2);
-        }
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          if (!WIDE && (c & 1) != hw) continue;
-          uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          if constexpr (Q8)
-            v = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f), pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
-                           pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f), pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * 128 * 128 + ((c ^ lrow) & 7) * 16)),
-                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
         }
         if (tid < TR_MAX_DRAFT_WORDS) bad[tid] = 0u;
         fence_proxy_async_shared();

@@ -444,6 +444,10 @@ TREES += [("bf16", "bf16", 128, 4, 100, 200, "bf16"), ("bf16", "bf16", 64, 8, 70
           ("bf16", "bf16", 64, 2, 256, 260, "bf16"), ("bf16", "bf16", 128, 4, 5, 3000, "f32"), ("e4m3", "bf16", 128, 4, 24, 1500, "f32")]
 
 
+TREES += [("int8", "f32", 128, 4, 16, 700, "f32"), ("e4m3", "f32", 128, 8, 40, 333, "bf16"), ("int8", "f32", 64, 2, 5, 4000, "f32"),
+          ("e4m3", "f32", 64, 8, 100, 90, "bf16"), ("int8", "f32", 128, 1, 1, 4097, "f32")]
+
+
 @pytest.mark.parametrize("kv, q, d, G, T, N, out", TREES)
 def test_tree_decode(api, lib, kv, q, d, G, T, N, out):
     B, Hkv = 2, 2
@@ -488,7 +492,7 @@ def test_tree_decode_chain_and_hidden_drafts(api, kv):
 @pytest.mark.parametrize("T, G, out", [(20, 1, "bf16"), (20, 4, "bf16"), (20, 8, "bf16"), (40, 8, "bf16"), (20, 4, "f32"), (7, 2, "f32"),
                                        (30, 5, "f32")])
 @pytest.mark.parametrize("kv", ["bf16", "int8", "e4m3"])
-def test_tree_decode_hidden_drafts_of_any_size(api, kv, T, G, out):
+def test_tree_decode_hidden_drafts_of_any_size(api, kv, T, G, out, q="bf16"):
     """Drafts 2^100 times the others' size do not change what the tokens that do not see them get."""
     B, Hkv, d, N = 1, 2, 128, 150
     K, V, sc, Kd, Vd = make_cache(kv, 95, B, Hkv, up(N + T), d)
@@ -498,13 +502,18 @@ def test_tree_decode_hidden_drafts_of_any_size(api, kv, T, G, out):
         V[:, :, big] *= 2.0**100
     else:
         sc[:, :, big] *= 2.0**100
-    Q = query(8, "bf16", B, T, Hkv * G, d)
+    Q = query(8, q, B, T, Hkv * G, d)
     seen = torch.zeros(B, T, T, dtype=torch.bool)
     seen[:, :, ::2] = torch.tril(torch.ones(T, T, dtype=torch.bool))[:, ::2]
     O = torch.empty(B, T, Hkv * G, d, dtype=QT[out], device=DEV)
     api.tree_decode(Q, K, V, N, 0.1, O, scales=sc, mask=api.tree_mask(seen).to(DEV))
     want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: list(range(N)) + [N + i for i in range(T) if seen[b, t, i]], 0.1)
     hold(O, want, A, S, d, N + T, out)
+
+
+@pytest.mark.parametrize("kv", ["int8", "e4m3"])
+def test_tree_decode_hidden_drafts_under_f32_queries(api, kv):
+    test_tree_decode_hidden_drafts_of_any_size(api, kv, 20, 4, "f32", q="f32")
 
 
 def test_tree_of_one_token_is_quant_decode(api):
