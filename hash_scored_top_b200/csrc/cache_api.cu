@@ -122,8 +122,8 @@ int tree_groups(int R, bool wide) { return wide ? (R + 255) / 256 : (R + 127) / 
 
 // Copies of the rows that share 128 rows of an MMA, at most. bf16 caches and f32
 // outputs: they hold the three terms of the weights (two products for 64 rows, one
-// for 32). 8-bit caches: two, for the two terms, or, with bf16 outputs, to share a
-// tile's keys, which keeps the softmax threads of all lanes busy.
+// for 32). 8-bit caches: two, which share a tile's keys, so that the softmax threads
+// of all lanes are busy.
 int tree_copies(int R) { return R > 64 ? 1 : R > 32 ? 2 : 4; }
 
 // Partials: (blocks + units) runs of one or two teams', or copies', rows.
@@ -219,7 +219,7 @@ template <int D, int FMT>
 int tree_attend(const CacheAttendParams& a, sk_dtype q, int B, void* O, sk_dtype o, cudaStream_t s) {
   const int R = a.T * a.G;
   if constexpr (FMT != KV_BF16) {
-    constexpr int KT = D == 128 ? 64 : 128;
+    constexpr int KT = 64;                                 // (two Q tiles of D = 128 leave no room for tiles of 128 keys)
     if (q == SK_F32)
       return o == SK_F32 ? launch_tree<D, KT, 2, false, 1, FMT, true>(a, B, reinterpret_cast<float*>(O), s)
                          : launch_tree<D, KT, 2, false, 1, FMT, true>(a, B, reinterpret_cast<__nv_bfloat16*>(O), s);

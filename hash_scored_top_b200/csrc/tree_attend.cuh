@@ -40,8 +40,10 @@
 // a power of two per row. A key's scale multiplies its column of S, a value's its
 // weights, which are kept below 2^15 by the largest exponent of a value scale so
 // far, as in stream_attend.cuh; one f16 term (11 bits) for bf16 outputs, two (22) for f32.
+// With R <= 64 the two copies of the rows share a tile's keys there (16 tokens of 4 heads over
+// 102384 int8 keys, 32 pairs, f32 outputs: 348 us; with a term of the weights to each copy 552).
 // f32 queries are two f16 tiles, high and low parts, whose products with K add up in S
-// (with D = 128 over tiles of 64 keys, to make room).
+// (over tiles of 64 keys, to make room).
 //
 // The list of all (pair, group of rows, tile) is cut into one even run per
 // block, as in stream_attend.cuh; a run that crosses a unit's end gives a partial for
@@ -190,8 +192,8 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
 // The value that a bf16 of x's upper half has: x cut off to 8 bits.
 __device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
-// NT terms of the weights in COPIES copies of the rows. With one term the copies share the keys instead: each takes half
-// of a tile's, with a maximum, a sum and an O of its own, and its weights for the others are 0.
+// NT terms of the weights in COPIES copies of the rows. Over 8-bit caches the (two) copies share the keys instead: each takes
+// half of a tile's, with a maximum, a sum and an O of its own, and its weights for the others are 0.
 template <int D, int KT, int NT, bool WIDE, int COPIES, int FMT, bool QF32 = false>
 __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::THREADS, 1)
     tree_attend_kernel(const TreeParams p, int B, const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV) {
@@ -201,7 +203,8 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
   constexpr int NS = SH::SLOTS, NR = SH::RAWS, ATOMS = D / 64, TEAMS = WIDE ? 2 : 1, TEAM = WIDE ? 128 : 256;
   // tensor memory: O of team w at w * D; buffer sb of its S (and P over it) behind them. Chunk q of 32 keys holds S at
   // 32 q, then P of the first two products at 32 q and 32 q + 16, of the third at KT + 16 q.
-  constexpr int NP = (NT + COPIES - 1) / COPIES;           // products per tile
+  constexpr bool SPLIT = Q8 && COPIES == 2;
+  constexpr int NP = SPLIT ? NT : (NT + COPIES - 1) / COPIES;      // products per tile
   constexpr uint32_t SCOLS = NP == 3 ? KT + KT / 2 : KT;
   static_assert(!WIDE || COPIES == 1, "a team has all its rows");
   // f32 outputs: O is added to a second one, which the MMAs do not touch, after every FLUSH tiles
@@ -459,8 +462,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    constexpr bool SPLIT = NT == 1 && COPIES == 2;         // (8 bits only)
-    static_assert(NT > 1 || COPIES == 1 || (SPLIT && Q8), "copies");
+    static_assert(COPIES == 1 || SPLIT || NT == 3, "copies");
     constexpr int COLS = WIDE ? KT : KT / (SPLIT ? 4 : 2), NQ = COLS / 32;      // columns of a tile per thread
     static_assert(COLS == 32 || COLS == 64, "a thread's columns");
     constexpr int OC = WIDE ? D : D / 2;                   // columns of O that it looks after
@@ -797,21 +799,17 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
               }
             }
             const uint32_t at = ts + 32u * (chunk0 + q);
-            if constexpr (NT == 1) {
+            if constexpr (NT < 3) {
               tmem_st16(at, t0);
+              if constexpr (NT == 2) tmem_st16(at + 16u, t1v);
               if constexpr (SPLIT) {
                 uint32_t none[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) none[k] = 0u;
-                tmem_st16(ts + 32u * (chunk0 ^ 2), none);  // the same share of the other copy's keys
+                const uint32_t others = ts + 32u * (chunk0 ^ 2);         // the same share of the other copy's keys
+                tmem_st16(others, none);
+                if constexpr (NT == 2) tmem_st16(others + 16u, none);
               }
-            } else if constexpr (NT == 2 && COPIES == 1) {
-              tmem_st16(at, t0);
-              tmem_st16(at + 16u, t1v);
-            } else if constexpr (NT == 2) {                // high | low
-#pragma unroll
-              for (int k = 0; k < 16; ++k) t0[k] = copy == 0 ? t0[k] : t1v[k];
-              tmem_st16(at, t0);
             } else if constexpr (COPIES == 1) {
               tmem_st16(at, t0);
               tmem_st16(at + 16u, t1v);
