@@ -517,14 +517,13 @@ def _addresses(device: int, *tensors):
         raise ValueError("tensors must live on a CUDA device")
     out = []
     for t in tensors:
-        if t is None:
-            out.append(None)
-        elif t.get_device() != device:
-            raise ValueError(f"tensors on cuda:{device} and {t.device}: one device expected")
-        elif not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        else:
-            out.append(t.data_ptr())
+        if t is not None:
+            if t.get_device() != device:
+                raise ValueError(f"tensors on cuda:{device} and {t.device}: one device expected")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            t = t.data_ptr()
+        out.append(t)
     return out
 
 
@@ -546,15 +545,16 @@ def _need(t, dtype, shape, name):
         _want(t, dtype, shape, name)
 
 
-def _want_cache(K, V, scales, quantised: bool = False):
-    """Checks K, V and their scales; returns the cache's dtype code."""
+def _want_cache(K, V, scales, shape, quantised: bool = False):
+    """Checks K, V (if any) and their scales against the cache's shape; returns the cache's dtype code."""
     code = _cache_code(K, quantised)
+    _need(K, K.dtype, shape, "K")
     if V is not None:
-        _need(V, K.dtype, K.shape, "V")
+        _need(V, K.dtype, shape, "V")
     if code >= SK_INT8:
         if scales is None:
             raise ValueError("scales: a quantised cache needs them")
-        _need(scales, torch.float32, (*K.shape[:3], 2), "scales")
+        _need(scales, torch.float32, (shape[0], shape[1], shape[2], 2), "scales")
     elif scales is not None:
         raise ValueError(f"scales: a {K.dtype} cache has none")
     return code
@@ -575,7 +575,7 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     (or starts[b] ..) of a quantised cache (see the C header)."""
     B, Hkv, Ncap, d = Kq.shape
     n = K_new.shape[2]
-    code = _want_cache(Kq, Vq, scales, quantised=True)
+    code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
     _need(K_new, K_new.dtype, (B, Hkv, n, d), "K_new")
     _need(V_new, K_new.dtype, (B, Hkv, n, d), "V_new")
     _want_lens(starts, B, "starts")
@@ -599,7 +599,7 @@ def quant_read(Kq, Vq, scales, K, V, n_begin: int = 0, starts=None, lens=None):
     """Reads rows n_begin .. (or starts[b] ..) of a quantised cache back into K, V [B, Hkv, n, d] (f32 or bf16)."""
     B, Hkv, Ncap, d = Kq.shape
     n = K.shape[2]
-    code = _want_cache(Kq, Vq, scales, quantised=True)
+    code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
     _need(K, K.dtype, (B, Hkv, n, d), "K")
     _need(V, K.dtype, (B, Hkv, n, d), "V")
     _want_lens(starts, B, "starts")
@@ -613,8 +613,7 @@ def quant_decode(Q, Kq, Vq, scales, N: int, scale: float, O, lens=None, ws=None)
     """Dense decode attention over a quantised cache: O [B, Hq, d] f32 (see the C header)."""
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
-    code = _want_cache(Kq, Vq, scales, quantised=True)
-    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
     _need(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
     i = Q.get_device()
@@ -628,8 +627,7 @@ def quant_sparse_attend(Q, Kq, Vq, scales, idx, scale: float, O, ws=None):
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
     k = idx.shape[-1]
-    code = _want_cache(Kq, Vq, scales, quantised=True)
-    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
     _need(idx, torch.int32, (B, Hkv, k), "idx")
     _need(O, torch.float32, (B, Hq, d), "O")
     i = Q.get_device()
@@ -643,8 +641,7 @@ def socket_decode_quant(Q, Kq, Vq, scales, R, ids, norms, N: int, L: int, P: int
     """socket_decode over a quantised K/V cache (the hashed-key cache as there): O [B, Hq, d] f32."""
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = Kq.shape
-    code = _want_cache(Kq, Vq, scales, quantised=True)
-    _need(Kq, Kq.dtype, (B, Hkv, Ncap, d), "Kq")
+    code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
     _need(R, torch.bfloat16, (L * P, d), "R")
     _need(ids, torch.uint8, (B, Hkv, Ncap, ids_bytes_per_key(L)), "ids")
     _need(norms, torch.float16, (B, Hkv, Ncap), "norms")
@@ -662,7 +659,7 @@ def block_summarize(K, block: int, bsum, n_begin: int = 0, n_count: int | None =
     """Summaries (per-channel minima and maxima) of the blocks that hold rows [n_begin, n_begin + n_count) of each pair."""
     B, Hkv, Ncap, d = K.shape
     n_count = Ncap - n_begin if n_count is None else n_count
-    code = _want_cache(K, None, scales)
+    code = _want_cache(K, None, scales, (B, Hkv, Ncap, d))
     _need(bsum, torch.bfloat16, (B, Hkv, -(-Ncap // block) if block > 0 else 0, 2, d), "bsum")
     _want_lens(starts, B, "starts")
     _want_lens(lens, B)
@@ -695,8 +692,7 @@ def block_attend(Q, K, V, N: int, block: int, idx, scale: float, O, scales=None,
     B, Hq, d = Q.shape
     _, Hkv, Ncap, _ = K.shape
     k = idx.shape[-1]
-    code = _want_cache(K, V, scales)
-    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    code = _want_cache(K, V, scales, (B, Hkv, Ncap, d))
     _need(idx, torch.int32, (B, Hkv, k), "idx")
     _need(O, torch.float32, (B, Hq, d), "O")
     _want_lens(lens, B)
@@ -712,8 +708,7 @@ def block_decode(Q, K, V, bsum, N: int, block: int, k: int, n_first: int, n_last
     """block_select, then block_attend over its choice: O [B, Hq, d] f32; idx_out [B, Hkv, k] int32 if given."""
     Ncap = K.shape[2]
     B, Hq, Hkv, d = _block_shapes(Q, bsum, Ncap, block)
-    code = _want_cache(K, V, scales)
-    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    code = _want_cache(K, V, scales, (B, Hkv, Ncap, d))
     _need(O, torch.float32, (B, Hq, d), "O")
     if idx_out is not None:
         _need(idx_out, torch.int32, (B, Hkv, k), "idx_out")
@@ -730,8 +725,7 @@ def tree_decode(Q, K, V, N: int, scale: float, O, mask=None, scales=None, lens=N
     chain), its drafted keys behind them: O [B, T, Hq, d] f32 or bf16 (see the C header)."""
     B, T, Hq, d = Q.shape
     _, Hkv, Ncap, _ = K.shape
-    code = _want_cache(K, V, scales)
-    _need(K, K.dtype, (B, Hkv, Ncap, d), "K")
+    code = _want_cache(K, V, scales, (B, Hkv, Ncap, d))
     _need(O, O.dtype, (B, T, Hq, d), "O")
     if mask is not None:
         _need(mask, torch.int32, (B, T, -(-T // 32)), "mask")
