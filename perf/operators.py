@@ -160,10 +160,9 @@ def prepare(case, seed):
     G = c["G"]
     Hq = Hkv * G
     Q = torch.randn(B, T, Hq, d, generator=gen, device="cuda").to(BF16)
-    # some keys, one in each sixteenth of the cache, point along a query of their group: they carry most of the weight
+    # some keys point along a query of their group: they carry most of the weight
     q = Q[:, 0].float().view(B, Hkv, G, d)[:, :, 0]
-    at = torch.arange(16, device="cuda") * N // 16 + torch.randint(0, N // 16, (B, Hkv, 16), generator=gen, device="cuda")
-    at = at[..., None].expand(B, Hkv, 16, d)
+    at = torch.randint(0, N, (B, Hkv, 16), generator=gen, device="cuda")[..., None].expand(B, Hkv, 16, d)
     needle = torch.randn(B, Hkv, 16, d, generator=gen, device="cuda") + 2.0 * (math.sqrt(d) * q / q.norm(dim=-1, keepdim=True))[:, :, None]
     K.scatter_(2, at, needle.to(BF16))
     s["Q"] = Q if drafts else Q[:, 0].contiguous()
