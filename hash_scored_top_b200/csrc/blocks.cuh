@@ -344,11 +344,12 @@ __global__ void __launch_bounds__(BSEL_THREADS) block_select_kernel(const BlockS
     int bits = 32 - __clz((int)(hi - lo));                 // keys lo .. lo + 2^bits - 1
     for (;;) {
       const int sh = max(bits - 11, 0);
+      const uint32_t bins = 1u << (bits - sh);             // of the range: the keys behind it were counted by the pass before
       for (int i = threadIdx.x; i < 2048; i += BSEL_THREADS) hist_s[i] = 0u;
       __syncthreads();
       each([&](int, uint32_t u) {
         const uint32_t d = (u - lo) >> sh;
-        if (u != 0xffffffffu && u >= lo && d < 2048u) atomicAdd(&hist_s[d], 1u);
+        if (u != 0xffffffffu && u >= lo && d < bins) atomicAdd(&hist_s[d], 1u);
       });
       __syncthreads();
       uint32_t c[4], sum = 0u;                             // bins 2047 - 4 thread downwards

@@ -1,0 +1,57 @@
+"""Edges of the operators over quantised, block-selected and drafted caches: choices where scores lie close together or are
+not finite, numbers near the ends of their types, codes that are no numbers. Tolerances: test_gpu_cache_ops.py."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ref as cr
+from tests.test_gpu_cache_ops import DEV, FMT, QT, api, choose, hold, lib, make_cache, oracle, query, rows, status, up  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- the choice of blocks
+def planted(values):
+    """f32 scores [B, Hkv, nb] -> (Q, bsum) that have them: three bf16 terms of each value in channels whose query is 1."""
+    B, Hkv, nb = values.shape
+    bsum = torch.zeros(B, Hkv, nb, 2, 64)
+    left = values.clone()
+    for c in range(3):
+        term = (left.view(torch.int32) & -65536).view(torch.float32)         # cut off to bf16: exact, and so is what is left
+        bsum[..., c] = term[..., None]
+        left = left - term
+    assert (left == 0).all()
+    Q = torch.zeros(B, Hkv, 64)
+    Q[..., :3] = 1.0
+    return Q.to(DEV), bsum.to(torch.bfloat16).to(DEV)
+
+
+@pytest.mark.parametrize("nb, k", [(1000, 100), (1500, 62), (4500, 300)])
+@pytest.mark.parametrize("base", [700.0, 1000.0, -3.0])
+def test_block_select_over_every_width_of_range(api, nb, k, base):
+    """Distinct scores, and many equal ones, in a range of 2^w steps of an f32, w from 1 to 23: each pass of the search, and
+    the second look at scores that f32 sums cannot tell apart, over ranges that are no multiple of a pass's bins."""
+    g = torch.Generator().manual_seed(nb + k)
+    for w in range(1, 24):
+        start = torch.tensor(base).view(torch.int32) - (1 << (w - 1))
+        v = (start + torch.randint(0, 1 << w, (2, 2, nb), generator=g, dtype=torch.int32)).view(torch.float32)
+        v[1, 0, ::2] = v[1, 0, nb // 2]                                      # half of them equal
+        v[1, 1] = v[1, 1].sort()[0]
+        Q, bsum = planted(v)
+        choose(api, Q, bsum, 16 * nb, 16, k, 1, 1)
+
+
+@pytest.mark.parametrize("block, N, k, spread", [(64, 131072, 100, 5.0), (64, 32768, 62, 5.0), (32, 102400, 97, 16.0), (16, 16000, 100, 1.0)])
+def test_block_select_of_scores_with_a_common_part(api, block, N, k, spread):
+    """Summaries that share a large channel, as keys with one strong channel do: all scores within part of one power of two."""
+    B, Hkv, G, d, nb = 2, 4, 8, 128, N // block
+    g = torch.Generator().manual_seed(N + k)
+    b = (torch.randn(B, Hkv, nb, 2, d, generator=g).sort(3)[0]).to(torch.bfloat16)
+    Q = query(k, "bf16", B, Hkv * G, d)
+    s = np.stack([cr.block_scores(Q[0, :G].double().cpu().numpy(), b[0, 0].double().numpy())])
+    Q = (Q.float() * (spread / float(s.std()))).to(torch.bfloat16)
+    b[..., 0], Q[..., 0] = 11.0, 8.0                                         # 8 heads x 88
+    choose(api, Q, b.to(DEV), N, block, k, 1, 1)
