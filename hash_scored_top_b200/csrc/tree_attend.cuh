@@ -59,7 +59,8 @@
 // per row. A V row that is not finite must reach only the rows that see it,
 // which a product cannot do (0 * NaN): such rows (and the rows behind the
 // sequence) are cleared in shared memory, and what a drafted one gives to the
-// rows that see it is added at the end, in plain arithmetic.
+// rows that see it is added at the end, in plain arithmetic. (e4m3: its NaN codes
+// alone are cleared, and make that column NaN for the rows that see them.)
 #pragma once
 
 #include <type_traits>
@@ -189,6 +190,14 @@ __device__ __forceinline__ uint64_t lds_f32x2(uint32_t addr) {
   return v;
 }
 
+// Clears the NaN codes among 16 e4m3 codes; whether there were any.
+__device__ __forceinline__ bool drop_nan_codes(uint4& v) {
+  const uint32_t x = __vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu), y = __vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  const uint32_t z = __vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu), w = __vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  v = make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~w);
+  return (x | y | z | w) != 0u;
+}
+
 // The value that a bf16 of x's upper half has: x cut off to 8 bits.
 __device__ __forceinline__ float cut_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 
@@ -216,6 +225,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
   extern __shared__ __align__(1024) unsigned char dyn[];
   __shared__ __align__(8) uint64_t bars[2 * TR_MAX_SLOTS + 16 + (Q8 ? 16 : 0)];
   __shared__ float vmax_s[4][4];                           // 8 bits: the largest value scale of a tile, by quarters of its rows
+  __shared__ uint32_t nan_s;                               // e4m3: set once a drafted row of V has a NaN code
   // drafted keys whose V was cleared, by the parity of the segment: they are cleared for a segment while others may
   // still read the last one's
   __shared__ uint32_t bad_s[2][TR_MAX_DRAFT_WORDS];
@@ -233,6 +243,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
     tmem_relinquish();
   }
   if (tid == 0) {
+    nan_s = 0u;
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, Q8 ? 128 : 1);
       mbar_init(empty + 8 * i, TEAMS);                     // one commit per team
@@ -437,6 +448,15 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
               uint4 v[AT_ONCE];
 #pragma unroll
               for (int x = 0; x < AT_ONCE; ++x) v[x] = lds128(src + 16u * (ct + 128 * (x0 + x)));
+              if constexpr (FMT == KV_E4M3) {              // NaN codes of drafted values stay out of the product
+                if (kv == 1 && (i + 1) * KT > seg.len) {
+#pragma unroll
+                  for (int x = 0; x < AT_ONCE; ++x) {
+                    const int row = (ct + 128 * (x0 + x)) / CR;
+                    if (i * KT + row >= seg.len && row < rows && drop_nan_codes(v[x])) atomicOr(&nan_s, 1u);
+                  }
+                }
+              }
 #pragma unroll
               for (int x = 0; x < AT_ONCE; ++x) {
                 const int piece = ct + 128 * (x0 + x), row = piece / CR, c = piece % CR;
@@ -900,6 +920,23 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
 #pragma unroll
           for (int k = 0; k < 32; k += 2) *reinterpret_cast<uint2*>(out + 2 + col + k) = make_uint2(o[k], o[k + 1]);
         }
+      }
+      if constexpr (FMT == KV_E4M3) {                      // rare: a weight times a NaN, for the rows that see its key
+        if (nan_s != 0u && live) {
+          int unit = seg.unit, r = my_row;                 // all else anew: kept in registers up to here it cost the tiles 2 to 3%
+          asm volatile("" : "+r"(unit), "+r"(r));
+          const int pair = unit / p.groups, b = pair / a.Hkv, len = seq_len(a.lens, b, a.N), col = WIDE ? 0 : hw * OC;
+          const TreeRow sees = {a.mask ? a.mask + ((size_t)b * a.T + r / a.G) * a.mask_words : nullptr, r / a.G, len, a.T};
+          const unsigned char* vp = reinterpret_cast<const unsigned char*>(a.V) + ((size_t)pair * a.Ncap + len) * D + col;
+#pragma unroll 1
+          for (int i = 0; i < a.T; ++i, vp += D) {
+            if (!((sees.drafts(i >> 5) >> (i & 31)) & 1u)) continue;
+#pragma unroll 1
+            for (int c = 0; c < OC; ++c)
+              if ((vp[c] & 0x7f) == 0x7f) out[2 + col + c] = __uint_as_float(0x7fc00000u);
+          }
+        }
+        __syncwarp();
       }
       if (row < p.rows && !idle && (WIDE || hw == 0)) *reinterpret_cast<float2*>(out) = make_float2(m, l);
       tc_fence_before_sync();                              // O has been read before the next segment's products

@@ -55,3 +55,35 @@ def test_block_select_of_scores_with_a_common_part(api, block, N, k, spread):
     Q = (Q.float() * (spread / float(s.std()))).to(torch.bfloat16)
     b[..., 0], Q[..., 0] = 11.0, 8.0                                         # 8 heads x 88
     choose(api, Q, b.to(DEV), N, block, k, 1, 1)
+
+
+# ---------------------------------------------------------------- numbers near the ends of their types, and codes that are none
+@pytest.mark.parametrize("T, G, d, q, out", [(20, 1, 128, "bf16", "bf16"), (20, 4, 64, "bf16", "f32"), (7, 2, 128, "bf16", "f32"), (20, 8, 128, "bf16", "bf16"),
+                                             (100, 8, 128, "bf16", "bf16"), (40, 4, 128, "bf16", "f32"), (20, 4, 128, "f32", "f32"), (100, 1, 64, "f32", "bf16")])
+def test_drafts_whose_codes_are_no_numbers(api, lib, T, G, d, q, out):
+    """e4m3 codes 0x7f and 0xff in drafted rows: the tokens that see the row have NaN in that channel, nobody else has one."""
+    B, Hkv, N = 2, 2, 150
+    K, V, sc, Kd, Vd = make_cache("e4m3", 98, B, Hkv, up(N + T), d)
+    lens = torch.tensor([N, N - 90], dtype=torch.int32, device=DEV)
+    seen = torch.zeros(B, T, T, dtype=torch.bool)
+    seen[:, :, ::2] = torch.tril(torch.ones(T, T, dtype=torch.bool))[:, ::2]
+    seen[:, 5, 5] = True
+    Kd, Vd = Kd.copy(), Vd.copy()
+    for b in range(B):
+        for i in range(1, T, 2):                                             # nobody sees the odd drafts, but for number 5
+            r = int(lens[b]) + i
+            V.view(torch.uint8)[b, :, r, i % d] = 0x7F
+            V.view(torch.uint8)[b, :, r, (3 * i + 64) % d] = 0xFF
+            Vd[b, :, r, i % d] = Vd[b, :, r, (3 * i + 64) % d] = np.nan
+            if i != 5:
+                K.view(torch.uint8)[b, :, r, (7 * i) % d] = 0xFF
+                Kd[b, :, r, (7 * i) % d] = np.nan
+    Q = query(10, q, B, T, Hkv * G, d)
+    O = torch.empty(B, T, Hkv * G, d, dtype=QT[out], device=DEV)
+    api.tree_decode(Q, K, V, N, 0.1, O, mask=api.tree_mask(seen).to(DEV), scales=sc, lens=lens)
+    want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: list(range(int(lens[b]))) + [int(lens[b]) + i for i in range(T) if seen[b, t, i]], 0.1)
+    none = np.isnan(want)
+    assert none[:, 5].sum() == 2 * B * Hkv * G and none.sum() == none[:, 5].sum()
+    assert np.array_equal(torch.isnan(O).cpu().numpy(), none)
+    hold(torch.nan_to_num(O.float()), np.nan_to_num(want), np.nan_to_num(A), S, d, N + T, out)
+    assert status(lib) == 0
