@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
 
       // ---- weights of head r for the keys 2c, 2c + 1 of each group
       constexpr int NW = 4 * HALVES;
-      float s[NW], vs[B16 ? 1 : NW];
+      float s[NW], ks[B16 ? 1 : NW], vs[B16 ? 1 : NW];
       int e = E;
 #pragma unroll
       for (int n = 0; n < 2 * HALVES; ++n) {
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
 #pragma unroll
         for (int n = 0; n < 2 * HALVES; ++n) {             // (scale of K, scale of V) of two rows
           const uint4 x = lds128(ssrc + (uint32_t)((n >> 1) * SH::HALF) + 64u * (n & 1));
-          s[2 * n] *= __uint_as_float(x.x);
-          s[2 * n + 1] *= __uint_as_float(x.z);
+          ks[2 * n] = __uint_as_float(x.x) * qscale;       // (S times either alone may leave f32 where the logit does not)
+          ks[2 * n + 1] = __uint_as_float(x.z) * qscale;
           vs[2 * n] = __uint_as_float(x.y);
           vs[2 * n + 1] = __uint_as_float(x.w);
           vm = fmaxf(vm, fmaxf(fabsf(vs[2 * n]), fabsf(vs[2 * n + 1])));
@@ -435,11 +435,11 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
       float mt = -INFINITY;
       if (live == (TILE == 32 ? 0xffffffffu : 0xffffu)) {
 #pragma unroll
-        for (int k = 0; k < NW; ++k) s[k] *= qscale;
+        for (int k = 0; k < NW; ++k) s[k] *= B16 ? qscale : ks[B16 ? 0 : k];
       } else {
         const uint32_t my = live >> (2 * c);
 #pragma unroll
-        for (int k = 0; k < NW; ++k) s[k] = (my >> ((k & 1) + 8 * (k >> 1))) & 1u ? s[k] * qscale : -INFINITY;
+        for (int k = 0; k < NW; ++k) s[k] = (my >> ((k & 1) + 8 * (k >> 1))) & 1u ? s[k] * (B16 ? qscale : ks[B16 ? 0 : k]) : -INFINITY;
       }
 #pragma unroll
       for (int k = 0; k < NW; ++k) mt = fmaxf(mt, s[k]);

@@ -668,19 +668,22 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
             vm = fmaxf(fmaxf(vmax_s[J & 3][0], vmax_s[J & 3][1]), fmaxf(vmax_s[J & 3][2], vmax_s[J & 3][3]));
           }
           e = max(E, (int)(__float_as_uint(vm) >> 23) - 127);
+          // from here on v holds the logits: S times the row's or the key's scale alone may leave f32 where they do not
+          const uint64_t rs2 = pack_f32x2(row_scale_log2, row_scale_log2);
 #pragma unroll
           for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float x, y;
-              unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])), lds_f32x2(kss + 128u * q + 4u * k)), x, y);
+              unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])), mul_f32x2(lds_f32x2(kss + 128u * q + 4u * k), rs2)), x, y);
               v[q][k] = __float_as_uint(x);
               v[q][k + 1] = __float_as_uint(y);
             }
         }
         // ---- the row's maximum
         float mt = -INFINITY;
-        if (!tail && a.scale_log2 >= 0.f) {
+        const float logit_scale = Q8 ? 1.f : row_scale_log2;
+        if (!tail && (Q8 || a.scale_log2 >= 0.f)) {
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             float x = __uint_as_float(v[q][0]), y = __uint_as_float(v[q][1]);      // two chains
@@ -691,13 +694,13 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
             }
             mt = max3(mt, x, y);
           }
-          mt *= row_scale_log2;
+          mt *= logit_scale;
         } else {                                           // masked, or an order that the scale turns round
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             const uint32_t see = vis.sees(jc + 32 * q);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * row_scale_log2 : -INFINITY);
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, (see >> k) & 1u ? __uint_as_float(v[q][k]) * logit_scale : -INFINITY);
           }
         }
         if constexpr (!WIDE) {
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
         // ---- weights, over the S that they come from
         auto weights = [&](auto mask_tag) {
           constexpr bool masked = decltype(mask_tag)::value;
-          const uint64_t sc2 = pack_f32x2(row_scale_log2, row_scale_log2), ms2 = pack_f32x2(-ms, -ms);
+          const uint64_t sc2 = pack_f32x2(logit_scale, logit_scale), ms2 = pack_f32x2(-ms, -ms);
           [[maybe_unused]] const uint64_t vf2 = pack_f32x2(vf, vf);
           uint64_t sum = 0ull;                             // (0, 0)
 #pragma unroll
@@ -790,7 +793,8 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float x, y;
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1])), sc2, ms2), x, y);
+              const uint64_t s2 = pack_f32x2(__uint_as_float(v[q][k]), __uint_as_float(v[q][k + 1]));
+              unpack_f32x2(Q8 ? add_f32x2(s2, ms2) : fma_f32x2(s2, sc2, ms2), x, y);
               x = ex2(x);
               y = ex2(y);
               if constexpr (masked) {

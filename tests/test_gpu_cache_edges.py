@@ -58,6 +58,39 @@ def test_block_select_of_scores_with_a_common_part(api, block, N, k, spread):
 
 
 # ---------------------------------------------------------------- numbers near the ends of their types, and codes that are none
+@pytest.mark.parametrize("fmt, q, d, G, T, out", [("int8", "bf16", 128, 4, 4, "f32"), ("e4m3", "f32", 64, 3, 1, "f32"), ("int8", "f32", 128, 8, 3, "bf16"),
+                                                  ("e4m3", "bf16", 128, 4, 20, "f32"), ("int8", "bf16", 64, 8, 20, "bf16")])
+def test_key_scales_of_any_size(api, fmt, q, d, G, T, out):
+    """Scales of seen keys up to 2^115, with queries that bring the logits back to ordinary size, and with ordinary ones, under
+    which the largest logit has all the weight."""
+    B, Hkv, N = 1, 2, 300
+    K, V, sc, Kd, Vd = make_cache(fmt, 97, B, Hkv, up(N + T), d)
+    base, k0 = query(9, "f32", B, T, Hkv * G, d), sc[..., 0].clone()
+    for qsize, ksize in ((2.0**-112, 2.0**112), (2.0**-100, 2.0**118), (2.0**110, 2.0**-110), (2.0**-20, 2.0**112), (1.0, 2.0**112)):
+        Q = (base * qsize).to(QT[q])
+        sc[..., 0] = k0 * ksize
+        scale = 0.1 if qsize * ksize < 2.0**30 else 1.0
+        if qsize * ksize == 2.0**18:
+            scale *= 2.0**-18
+        seen = lambda b, h, t: slice(0, N + t + 1)                           # noqa: E731
+        want, A, S = oracle(Q, Kd * ksize, Vd, seen, scale)
+        if S.max() > 1e6:                                                    # one key has all the weight, by far
+            for hq in range(Hkv * G):
+                x = np.sort(Q[0, -1, hq].double().cpu().numpy() @ (Kd[0, hq // G] * ksize)[:N + T].T)
+                assert x[-1] - x[-2] > 2.0**-12 * S[0, -1, hq]
+            S = np.zeros_like(S)
+        O = torch.empty(B, T, Hkv * G, d, dtype=QT[out], device=DEV)
+        api.tree_decode(Q, K, V, N, scale, O, scales=sc)
+        if S.max() == 0:
+            hold(O[:, -1:], want[:, -1:], A[:, -1:], S[:, -1:], d, N + T, out)
+            assert torch.isfinite(O.float()).all()
+        else:
+            hold(O, want, A, S, d, N + T, out)
+        O1 = torch.empty(B, Hkv * G, d, device=DEV)
+        api.quant_decode(Q[:, -1].contiguous(), K, V, sc, N + T, scale, O1)
+        hold(O1[:, None], want[:, -1:], A[:, -1:], S[:, -1:], d, N + T)
+
+
 @pytest.mark.parametrize("T, G, d, q, out", [(20, 1, 128, "bf16", "bf16"), (20, 4, 64, "bf16", "f32"), (7, 2, 128, "bf16", "f32"), (20, 8, 128, "bf16", "bf16"),
                                              (100, 8, 128, "bf16", "bf16"), (40, 4, 128, "bf16", "f32"), (20, 4, 128, "f32", "f32"), (100, 1, 64, "f32", "bf16")])
 def test_drafts_whose_codes_are_no_numbers(api, lib, T, G, d, q, out):
