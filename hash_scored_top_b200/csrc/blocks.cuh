@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(BSEL_THREADS) block_select_kernel(const BlockS
       float q[8];
       load8(Qg + g * D, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) T[i] += (double)(8 * piece < D ? fminf(q[i], 0.f) : fmaxf(q[i], 0.f));
+      for (int i = 0; i < 8; ++i) T[i] += (double)((8 * piece < D ? q[i] > 0.f : q[i] < 0.f) ? 0.f : q[i]);     // (a NaN stays one)
     }
   }
   uint64_t T2[4];                                          // as f32, and the magnitudes as bf16, rounded up

@@ -57,6 +57,21 @@ def test_block_select_of_scores_with_a_common_part(api, block, N, k, spread):
     choose(api, Q, b.to(DEV), N, block, k, 1, 1)
 
 
+def test_block_select_of_queries_that_are_no_numbers(api):
+    """A NaN in a query makes every score of its group NaN: the lowest blocks, and the forced ones."""
+    g = torch.Generator().manual_seed(9)
+    b = torch.randn(1, 2, 300, 2, 64, generator=g).sort(3)[0].to(torch.bfloat16).to(DEV)
+    for q in QT:
+        Q = query(3, q, 1, 8, 64)
+        Q[0, 2, 17] = math.nan                                               # the first group's
+        choose(api, Q, b, 4800, 16, 20, 1, 2)
+        idx = torch.empty(1, 2, 20, dtype=torch.int32, device=DEV)
+        api.block_select(Q, b, 4800, 4800, 16, 1, 2, idx)
+        assert idx[0, 0].tolist() == [*range(18), 298, 299]
+    Q[0, 2, 17] = math.inf
+    choose(api, Q, b, 4800, 16, 20, 1, 2)
+
+
 # ---------------------------------------------------------------- numbers near the ends of their types, and codes that are none
 @pytest.mark.parametrize("fmt, q, d, G, T, out", [("int8", "bf16", 128, 4, 4, "f32"), ("e4m3", "f32", 64, 3, 1, "f32"), ("int8", "f32", 128, 8, 3, "bf16"),
                                                   ("e4m3", "bf16", 128, 4, 20, "f32"), ("int8", "bf16", 64, 8, 20, "bf16")])
