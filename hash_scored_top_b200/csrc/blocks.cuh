@@ -146,6 +146,19 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
 
 __device__ __forceinline__ float ordered_value(uint32_t u) { return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u); }
 
+// The smaller and the larger; a NaN if either is one. (Comparisons and a choice in their place took the selection from 25.6 to
+// 28 us: the compiler made branches of them, and the heads' loads followed one another.)
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float v;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float v;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(a), "f"(b));
+  return v;
+}
+
 constexpr int BSEL_THREADS = 512;
 constexpr int BSEL_WARPS = BSEL_THREADS / 32;
 constexpr int BSEL_MAX_KEYS = 51200;         // a pair's keys in the first CTA's shared memory
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(BSEL_THREADS) block_select_kernel(const BlockS
       float q[8];
       load8(Qg + g * D, q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) T[i] += (double)((8 * piece < D ? q[i] > 0.f : q[i] < 0.f) ? 0.f : q[i]);     // (a NaN stays one)
+      for (int i = 0; i < 8; ++i) T[i] += (double)(8 * piece < D ? min_nan(q[i], 0.f) : max_nan(q[i], 0.f));
     }
   }
   uint64_t T2[4];                                          // as f32, and the magnitudes as bf16, rounded up
