@@ -6,6 +6,8 @@
 // q_c > 0 and q_c mn_c otherwise, so the bounds of a group's heads add up to
 // one product of length 2 D:
 //   score_b = T- . mn_b + T+ . mx_b,  T- = sum_h min(q_h, 0), T+ = sum_h max(q_h, 0).
+// That product is the definition, also of summaries that are not finite: an
+// infinite minimum or maximum where T- or T+ is 0 gives NaN.
 // The score is that of the sums in f64, rounded once to f32: which block is
 // chosen does not depend on the order of the sum, and equal f32 scores go to
 // the lower block.

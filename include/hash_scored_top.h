@@ -488,11 +488,16 @@ int block_summarize(const void* K, sk_dtype kv, const float* scales, const int* 
 
 /*
  * Chooses k blocks of each pair: the score of a block is
- *   sum over the group's query heads h of sum_c max(q_hc min_c, q_hc max_c),
- * the sum of the upper bounds on q_h . k that its summary gives, rounded once
- * to f32. The sequence's first n_first and last n_last blocks (the last may be
- * partly filled) are always in; the others by score, ties to the lower block,
- * a NaN score below all. idx [B][Hkv][k] int32: ascending, and -1 where a
+ *   sum over the channels c of Tneg_c min_c + Tpos_c max_c,
+ * Tneg_c and Tpos_c the sums of the negative and of the positive q_hc of the
+ * group's query heads h (0 where there are none, NaN where a q_hc is NaN),
+ * rounded once to f32. Of a finite summary that is the sum over h and c of
+ * max(q_hc min_c, q_hc max_c), the upper bounds on q_h . k that it gives. An
+ * infinite minimum (maximum) where Tneg_c (Tpos_c) is 0 makes the score NaN
+ * (0 * infinity), as infinities of both signs in the sum do. The sequence's
+ * first n_first and last n_last blocks (the last may be partly filled) are
+ * always in; the others by score, ties to the lower block, a NaN score below
+ * all. idx [B][Hkv][k] int32: ascending, and -1 where a
  * sequence has fewer than k blocks. Q [B][Hq][d]. Requires n_first + n_last <=
  * k. ws: sk_workspace_bytes(SK_OP_BLOCK_SELECT).
  */

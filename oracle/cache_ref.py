@@ -77,9 +77,11 @@ def block_summary(K, block: int, N: int) -> np.ndarray:
 
 def block_scores(Qg, bsum) -> np.ndarray:
     """Group scores [NB] (float32) of summaries [NB, 2, d] for the group's query rows Qg [G, d]."""
-    q = np.asarray(Qg, dtype=np.float64)[:, None]
-    b = np.asarray(bsum, dtype=np.float64)[None]
-    return np.maximum(q * b[:, :, 0], q * b[:, :, 1]).sum((0, 2)).astype(np.float32)
+    q = np.asarray(Qg, dtype=np.float64)
+    b = np.asarray(bsum, dtype=np.float64)
+    neg, pos = np.minimum(q, 0.0).sum(0), np.maximum(q, 0.0).sum(0)
+    with np.errstate(invalid="ignore", over="ignore"):       # 0 * infinity is NaN; sums may leave f32
+        return (neg * b[:, 0] + pos * b[:, 1]).sum(-1).astype(np.float32)
 
 
 def select_blocks(scores, nb: int, k: int, n_first: int, n_last: int) -> np.ndarray:

@@ -72,6 +72,26 @@ def test_block_select_of_queries_that_are_no_numbers(api):
     choose(api, Q, b, 4800, 16, 20, 1, 2)
 
 
+@pytest.mark.parametrize("G, d", [(1, 64), (4, 128), (8, 64)])
+def test_block_select_of_infinite_summaries(api, G, d):
+    """Infinite minima and maxima under queries of either sign, some of them 0: the definition's values, as they are."""
+    g = torch.Generator().manual_seed(G)
+    B, Hkv, nb = 2, 2, 120
+    Q = query(G, "bf16", B, Hkv * G, d)
+    Q[0, :, 3] = Q[0, :, 3].abs()
+    Q[0, :, 4] = -Q[0, :, 4].abs()
+    Q[1, :, 5] = 0.0
+    for n in (1, 10, 60, 120):
+        b = torch.randn(B, Hkv, nb, 2, d, generator=g).sort(3)[0].to(torch.bfloat16)
+        hit = torch.randperm(nb, generator=g)[:n]
+        for i, j in enumerate(hit.tolist()):
+            c = (3, 4, 5, 7)[i % 4]
+            b[:, :, j, 0 if i % 3 else 1, c] = -math.inf if i % 3 else math.inf
+            if i % 7 == 0:
+                b[:, :, j, :, 9] = torch.tensor([-math.inf, math.inf])
+        choose(api, Q, b.to(DEV), 16 * nb, 16, 25, 1, 1)
+
+
 # ---------------------------------------------------------------- numbers near the ends of their types, and codes that are none
 @pytest.mark.parametrize("fmt, q, d, G, T, out", [("int8", "bf16", 128, 4, 4, "f32"), ("e4m3", "f32", 64, 3, 1, "f32"), ("int8", "f32", 128, 8, 3, "bf16"),
                                                   ("e4m3", "bf16", 128, 4, 20, "f32"), ("int8", "bf16", 64, 8, 20, "bf16")])

@@ -57,6 +57,20 @@ def test_scores_bound_the_keys():
     assert np.array_equal(b[3], cr.block_summary(K[96:], 32, 4)[0])
 
 
+def test_scores_are_the_heads_bounds_where_finite():
+    rng = np.random.default_rng(6)
+    b, q = np.sort(rng.normal(size=(20, 2, 64)), axis=1), rng.normal(size=(3, 64))
+    q[0, 5] = 0.0
+    heads = np.maximum(q[:, None] * b[None, :, 0], q[:, None] * b[None, :, 1]).sum((0, 2))
+    assert np.allclose(cr.block_scores(q, b), heads, rtol=1e-6, atol=1e-6)
+    q[:, 7], q[:, 8], q[1, 8] = np.abs(q[:, 7]), -np.abs(q[:, 8]), 0.25
+    b[0, 1, 7], b[1, 0, 7], b[2, 1, 8], b[3, 0, 8] = math.inf, -math.inf, math.inf, -math.inf
+    s = cr.block_scores(q, b)
+    assert s[0] == math.inf and math.isnan(s[1]) and s[2] == math.inf and s[3] == math.inf      # (a negative query, -infinity)
+    q[1, 9] = math.nan
+    assert np.isnan(cr.block_scores(q, b)).all()
+
+
 def test_select_blocks_order():
     s = np.array([1.0, 5.0, 5.0, np.nan, 5.0, -2.0], np.float32)
     assert list(cr.select_blocks(s, 6, 2, 0, 0)) == [1, 2]
