@@ -420,6 +420,13 @@ int socket_soft_count_attend(const void* Q, const void* V, sk_dtype kv, const vo
  * Attention over a quantised cache holds a key's weight times its value's scale
  * to 22 bits, and to 2^-38 of the largest value scale that the query row sees:
  * values whose rows are that much smaller than another one's are lost beside it.
+ * f32 queries over it are held to 22 bits of the largest value of their row.
+ * The weighted sum of the values is held in f32, its weights at most 1
+ * (tree_decode: 2^8), before it is divided by the sum of the weights: the
+ * values' magnitude times the number of keys has to stay below 2^119. A value
+ * that a row sees makes its channel, and no other, NaN if it is one, and infinite
+ * or NaN if it is infinite (f32 caches: infinite). These caches are not paged: a
+ * sequence's rows lie one after another.
  * O is f32 unless said otherwise, its layout as Q's. G = Hq / Hkv <= 8 and
  * B * Hkv <= 65535 in all of them. ws, O and scales must be 16-byte aligned.
  */

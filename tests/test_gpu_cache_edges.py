@@ -155,3 +155,31 @@ def test_drafts_whose_codes_are_no_numbers(api, lib, T, G, d, q, out):
     assert np.array_equal(torch.isnan(O).cpu().numpy(), none)
     hold(torch.nan_to_num(O.float()), np.nan_to_num(want), np.nan_to_num(A), S, d, N + T, out)
     assert status(lib) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+def test_infinite_values_that_are_seen(api, kv):
+    """They show in their channel (infinite or NaN over bf16 caches, infinite over f32 ones) and in no other."""
+    B, Hkv, G, d, N, T = 1, 2, 4, 128, 300, 12
+    K, V, _, Kd, Vd = make_cache(kv, 99, B, Hkv, up(N + T), d)
+    V[0, :, 40, 7], V[0, :, N + 2, 9] = math.inf, -math.inf                  # a cached row, and a draft
+    Vd[0, :, 40, 7], Vd[0, :, N + 2, 9] = 0.0, 0.0
+    Q = query(11, kv, B, T, Hkv * G, d)
+    O = torch.empty(B, T, Hkv * G, d, device=DEV)
+    api.tree_decode(Q, K, V, N, 0.1, O)
+    want, A, S = oracle(Q, Kd, Vd, lambda b, h, t: slice(0, N + t + 1), 0.1)
+    bad = torch.zeros_like(O, dtype=torch.bool)
+    bad[..., 7] = True
+    bad[:, 2:, :, 9] = True
+    assert torch.equal(~torch.isfinite(O), bad)
+    assert (O[:, 2:, :, 9] == -math.inf).all()
+    if kv == "f32":
+        assert (O[..., 7] == math.inf).all()
+    at = bad.cpu().numpy()
+    hold(O.masked_fill(bad, 0.0), np.where(at, 0.0, want), np.where(at, 0.0, A), S, d, N + T)
+    bl = torch.tensor([1, 4], dtype=torch.int32, device=DEV).expand(B, Hkv, 2).contiguous()
+    O1 = torch.empty(B, Hkv * G, d, device=DEV)
+    api.block_attend(Q[:, 0].contiguous(), K, V, N, 32, bl, 0.1, O1)
+    want, A, S = oracle(Q[:, :1], Kd, Vd, lambda b, h, t: [*range(32, 64), *range(128, 160)], 0.1)
+    assert torch.equal(~torch.isfinite(O1), bad[:, 0])
+    hold(O1[:, None].masked_fill(bad[:, :1], 0.0), np.where(at[:, :1], 0.0, want), np.where(at[:, :1], 0.0, A), S, d, 64)
