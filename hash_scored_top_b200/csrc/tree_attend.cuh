@@ -72,7 +72,7 @@
 namespace hst {
 
 constexpr int TR_MAX_SLOTS = 12;
-constexpr uint32_t TR_SMEM_MAX = 231424;     // dynamic; 1 KB of static shared memory besides
+constexpr uint32_t TR_SMEM_MAX = 229376;     // dynamic; of a block's 232448, 3 KB are the kernel's static arrays
 constexpr int TR_MAX_DRAFT_WORDS = 8;
 
 template <int D, int KT, bool WIDE, bool Q8, bool QF32 = false>
@@ -89,6 +89,7 @@ struct TreeShape {
   static constexpr int RAWS = !Q8 ? 0 : RAW_FIT < 6 ? RAW_FIT : 6;
   static constexpr int SMEM = QTILES * QBYTES + SLOTS * SLOT + RAWS * RAW + (Q8 ? 4 * KT * 8 : 0);
   static_assert(Q8 ? RAWS >= 3 : SLOTS >= 6, "the tiles of both buffers and one in flight");
+  static_assert(SMEM <= (int)TR_SMEM_MAX, "dynamic shared memory");
 };
 
 struct TreeParams {
@@ -231,6 +232,8 @@ __global__ void __launch_bounds__(TreeShape<D, KT, WIDE, FMT != KV_BF16, QF32>::
   __shared__ uint32_t bad_s[2][TR_MAX_DRAFT_WORDS];
   __shared__ float half_s[2][2][128];                      // maxima (at the end sums) of half a row, by the parity of the tile
   __shared__ uint32_t tbase_s;
+  static_assert(sizeof(bars) + sizeof(vmax_s) + sizeof(nan_s) + sizeof(bad_s) + sizeof(half_s) + sizeof(tbase_s) <= 232448 - TR_SMEM_MAX,
+                "static shared memory");
   const CacheAttendParams& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
   const uint32_t s0 = smem_u32(dyn), q0 = s0, slots = s0 + SH::QTILES * SH::QBYTES;
