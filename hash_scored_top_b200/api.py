@@ -571,8 +571,8 @@ def _ws_arg(ws, op, Q, *shape):
 
 
 def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, lens=None):
-    """Quantises K_new, V_new [B, Hkv, n, d] (f32 or bf16; any strides, the last dimension contiguous) into rows n_begin ..
-    (or starts[b] ..) of a quantised cache (see the C header)."""
+    """Quantises K_new, V_new [B, Hkv, n, d] (f32 or bf16; the last dimension contiguous, the others' strides multiples of 16
+    bytes) into rows n_begin .. (or starts[b] ..) of a quantised cache (see the C header)."""
     B, Hkv, Ncap, d = Kq.shape
     n = K_new.shape[2]
     code = _want_cache(Kq, Vq, scales, (B, Hkv, Ncap, d), quantised=True)
@@ -587,6 +587,12 @@ def quant_append(K_new, V_new, Kq, Vq, scales, n_begin: int = 0, starts=None, le
     sb, sh, sn, sd = strides
     if sd != 1:
         raise ValueError("K_new, V_new: the last dimension must be contiguous")
+    if B == 1:
+        sb = 0
+    if Hkv == 1:
+        sh = 0
+    if n == 1:
+        sn = 0
     i = Kq.get_device()
     pk, pv, ps, p_starts, p_lens = _addresses(i, Kq, Vq, scales, starts, lens)
     if K_new.get_device() != i or V_new.get_device() != i:

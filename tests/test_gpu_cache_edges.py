@@ -183,3 +183,16 @@ def test_infinite_values_that_are_seen(api, kv):
     want, A, S = oracle(Q[:, :1], Kd, Vd, lambda b, h, t: [*range(32, 64), *range(128, 160)], 0.1)
     assert torch.equal(~torch.isfinite(O1), bad[:, 0])
     hold(O1[:, None].masked_fill(bad[:, :1], 0.0), np.where(at[:, :1], 0.0, want), np.where(at[:, :1], 0.0, A), S, d, 64)
+
+
+# ---------------------------------------------------------------- layouts
+def test_append_of_a_row_with_odd_strides(api):
+    """The stride of a dimension of one says nothing: a row that was computed as a column."""
+    Kq, Vq, sc = api.empty_quant(1, 1, 64, 128)
+    col = rows(1, 128, 1).to(DEV)
+    new = col.T[None, None]
+    assert new.stride()[:3] == (1, 1, 1)
+    api.quant_append(new, new, Kq, Vq, sc, n_begin=9)
+    c, s = cr.quantise(col[:, 0].double().cpu().numpy(), "int8")
+    for x, z in ((Kq, 0), (Vq, 1)):
+        assert np.array_equal(x[0, 0, 9].double().cpu().numpy(), c) and float(sc[0, 0, 9, z]) == float(s)
