@@ -43,14 +43,15 @@ __device__ __forceinline__ int seq_len(const int* lens, int b, int N) {
   return lens ? min(max(__ldg(lens + b), 0), N) : N;
 }
 
-// What position j of a pair is (but for KEYS_ALL): its cache row, or -1 when it is not seen.
+// What position j of a pair is (but for KEYS_ALL): its cache row, or -1 when it is not seen. The list may be the previous
+// kernel's, which still runs when this one starts, so it is not read as constant data (__ldg).
 __device__ __forceinline__ int key_row(const CacheAttendParams& p, int pair, int b, int t, int len, int j) {
   if (p.mode == KEYS_LISTED) {
-    const int r = __ldg(p.idx + (size_t)pair * p.k + j);
+    const int r = __ldcg(p.idx + (size_t)pair * p.k + j);
     return r >= 0 && r < p.Ncap ? r : -1;
   }
   if (p.mode == KEYS_BLOCKS) {
-    const int bl = __ldg(p.idx + (size_t)pair * p.k + j / p.block);
+    const int bl = __ldcg(p.idx + (size_t)pair * p.k + j / p.block);
     if (bl < 0 || bl > (len - 1) / p.block) return -1;
     const int r = bl * p.block + j % p.block;
     return r < len ? r : -1;

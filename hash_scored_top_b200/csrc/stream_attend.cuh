@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(StreamShape<D, FMT>::THREADS, 1) stream_attend
       if (t >= te || j >= a.n) return x;
       x.row = j;
       if (a.mode == KEYS_BLOCKS) {
-        const int bl = __ldg(a.idx + (size_t)pair * a.k + j / a.block);
+        const int bl = __ldcg(a.idx + (size_t)pair * a.k + j / a.block);
         if (bl < 0 || bl > (len - 1) / a.block) return x;
         x.row = bl * a.block + j % a.block;
       }
