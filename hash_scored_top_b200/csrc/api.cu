@@ -35,6 +35,7 @@ int hst::fail(int code, const char* fmt, ...) {
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
   g_last_error = buf;
+  if (code == SK_ERR_CUDA) cudaGetLastError();       // it is reported: the next call must not find it again
   return code;
 }
 

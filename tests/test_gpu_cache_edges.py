@@ -1,6 +1,7 @@
 """Edges of the operators over quantised, block-selected and drafted caches: choices where scores lie close together or are
 not finite, numbers near the ends of their types, codes that are no numbers. Tolerances: test_gpu_cache_ops.py."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -196,3 +197,26 @@ def test_append_of_a_row_with_odd_strides(api):
     c, s = cr.quantise(col[:, 0].double().cpu().numpy(), "int8")
     for x, z in ((Kq, 0), (Vq, 1)):
         assert np.array_equal(x[0, 0, 9].double().cpu().numpy(), c) and float(sc[0, 0, 9, z]) == float(s)
+
+
+# ---------------------------------------------------------------- errors
+def test_a_failed_launch_is_reported_once(api, lib):
+    """A launch into a capture that has become invalid fails; the calls after it do not report it again."""
+    driver = ctypes.CDLL("libcuda.so.1")
+    Kq, Vq, sc = api.empty_quant(1, 1, 64, 128)
+    new = rows(1, 1, 1, 2, 128).to(DEV)
+    O, Q = torch.empty(1, 1, 128, device=DEV), query(1, "bf16", 1, 1, 128)
+    ws = torch.empty(api.workspace_bytes(api.OP_QUANT_DECODE, 1, 1, 1, 64, 2, 128), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p()
+    assert driver.cuStreamBeginCapture_v2(handle, 2) == 0
+    assert driver.cuStreamSynchronize(handle) == 900                         # not allowed there: the capture is invalid now
+    with torch.cuda.stream(s):
+        with pytest.raises(RuntimeError, match="quant_append"):
+            api.quant_append(new, new, Kq, Vq, sc)
+        assert driver.cuStreamEndCapture(handle, ctypes.byref(graph)) == 901
+        api.quant_append(new, new, Kq, Vq, sc)
+        api.quant_decode(Q, Kq, Vq, sc, 2, 0.1, O, ws=ws)
+    s.synchronize()
+    assert (sc[0, 0, :2] > 0).all() and status(lib) == 0
