@@ -74,9 +74,9 @@ __device__ __forceinline__ float4 row_quad(const void* base, size_t row, int D, 
 
 constexpr int CACHE_THREADS = 256;
 
-// The simple kernel, for f32 caches: a warp per key. Bound by its instructions
-// (an int8 form of it took 2027 us for 102400 keys of 32 pairs, G = 4, which
-// stream_attend_kernel takes 118 for).
+// The simple kernel, for f32 caches: a warp per key. Bound by its instructions:
+// 97 chosen blocks of 32 keys, 32 pairs, G = 4, D = 128 take 92 us, where
+// stream_attend_kernel takes 16 for a bf16 cache.
 // grid = (splits, R, pairs); warp w takes the split's positions w, w + 8, ...
 // and its lanes the head dimension.
 template <int D>

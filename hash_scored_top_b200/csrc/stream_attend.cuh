@@ -32,9 +32,11 @@
 //     of a value scale so far, next to the running maximum, and enter as two
 //     f16 terms (22 bits). bf16 caches use bf16 products, weights in three
 //     terms (24 bits).
-// 102400 keys of 32 pairs, D = 128, G = 4: bf16 6.46 TB/s (a copy's rate), int8
-// 6.17, e4m3 5.6 (its conversions to f16); D = 64 8-bit rows 4.4 to 4.9, where the
-// work per byte is the largest. A short list (3103 rows a pair) is bound by latency: 19 us.
+// 102400 keys of 32 pairs, D = 128, G = 4: bf16 6.9 TB/s, int8 6.0, e4m3 5.4 (its
+// conversions to f16); D = 64 8-bit rows 4.5 to 4.9, where the work per byte is
+// the largest. Short lists (32 pairs of 3103 rows: 19 us, whose bytes take 4) pay
+// for what a block does once for a pair: the query, the first copies, the join of
+// its warps, each behind the last.
 #pragma once
 
 #include "cache_attend.cuh"

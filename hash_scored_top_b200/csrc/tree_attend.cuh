@@ -41,7 +41,8 @@
 // weights, which are kept below 2^15 by the largest exponent of a value scale so
 // far, as in stream_attend.cuh; one f16 term (11 bits) for bf16 outputs, two (22) for f32.
 // With R <= 64 the two copies of the rows share a tile's keys there (16 tokens of 4 heads over
-// 102384 int8 keys, 32 pairs, f32 outputs: 348 us; with a term of the weights to each copy 552).
+// 102384 int8 keys, 32 pairs, f32 outputs, in a loop: 348 us; with a term of the weights to each
+// copy 552. 305 alone).
 // f32 queries are two f16 tiles, high and low parts, whose products with K add up in S
 // (over tiles of 64 keys, to make room).
 //
@@ -50,10 +51,11 @@
 // each side, which tree_merge_kernel joins in order.
 //
 // Four sequences of up to 102400 keys, 8 KV heads of 4 queries, D = 128: 16 tokens with f32
-// outputs 282 us (4.8 TB/s; the tensor pipe 51% busy), 64 tokens with bf16 outputs 377 (the
+// outputs 283 us (4.8 TB/s; the tensor pipe 51% busy), 64 tokens with bf16 outputs 381 (the
 // exponentials and the products 50% each); in a loop the GPU's power limit makes that
-// 310 to 330 and 420 to 450. 7 tokens over int8, 32761 keys of 8 pairs: 46 us (the conversion,
-// about 3000 clocks a tile).
+// 310 to 330 and 420 to 450. 7 tokens over int8, 32761 keys of 8 pairs: 47 us (the conversion,
+// about 3000 clocks a tile), with f32 queries and outputs 63. The 8-bit kernels of one copy (R > 64,
+// or f32 queries) spill 8 to 232 bytes, most with f32 outputs: 448 threads leave 128 registers to each.
 //
 // Drafted keys lie behind the cached ones, in the last tiles. Their S is masked
 // per row. A V row that is not finite must reach only the rows that see it,
